@@ -28,6 +28,9 @@ __all__ = [
     "HQQError", "HQQParams", "lib", "library_path", "hqq_quantize", "hqq_quantize_ex",
     "hqq_dequantize", "hqq_dequantize_ex", "hqq_quantize_meta", "hqq_dequantize_meta",
     "hqq_packed_bytes", "hqq_num_groups", "hqq_num_meta_groups", "hqq_workspace_bytes",
+    "QuantizedWeight", "quantized_weight", "hqq_linear", "hqq_linear_ex", "hqq_linear_backward",
+    "hqq_gated_linear", "hqq_gated_linear_backward", "hqq_linear_workspace_bytes",
+    "hqq_gated_linear_workspace_bytes",
     "HQQ_F16", "HQQ_BF16", "HQQ_F32", "HQQ_U8",
 ]
 
@@ -64,6 +67,15 @@ class HQQParams(ctypes.Structure):
                 ("meta_dtype", ctypes.c_int), ("quant_scale", ctypes.c_int),
                 ("quant_zero", ctypes.c_int), ("meta_group_size", ctypes.c_int),
                 ("flags", ctypes.c_int)]
+
+
+class HQQWeight(ctypes.Structure):
+    """Mirror of the C struct hqq_weight (one quantized weight of a product)."""
+    _fields_ = [("Wq_packed", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("zero", ctypes.c_void_p), ("scale_mm", ctypes.c_void_p),
+                ("zero_mm", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("params", HQQParams)]
+
 
 HQQ_FLAG_STOP_AT_FIXED_POINT = 1
 HQQ_FLAG_OVERLAP_WEIGHTS = 2
@@ -108,6 +120,16 @@ def lib() -> ctypes.CDLL:
             L.hqq_dequantize_meta.argtypes = [P, P, i64, i32, P, P]
             L.hqq_linear.argtypes = [P, i64, i64, i32, P, P, P, P, i64,
                                      ctypes.POINTER(HQQParams), P, P]
+            W = ctypes.POINTER(HQQWeight)
+            L.hqq_linear_workspace_bytes.argtypes = [i64, W, i32]
+            L.hqq_gated_linear_workspace_bytes.argtypes = [i64, W, W, i32]
+            L.hqq_linear_ex.argtypes = [P, i64, i32, W, P, P, sz, P]
+            L.hqq_linear_backward.argtypes = [P, i64, i32, W, P, P, P, sz, P]
+            L.hqq_gated_linear.argtypes = [P, i64, i32, W, W, i32, P, P, P, P, sz, P]
+            L.hqq_gated_linear_backward.argtypes = [P, P, P, i64, i32, W, W, i32, P, P, P, P, P,
+                                                    P, sz, P]
+            for f in ("hqq_linear_workspace_bytes", "hqq_gated_linear_workspace_bytes"):
+                getattr(L, f).restype = sz
             L.hqq_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
             L.hqq_mxfp4_quantize.argtypes = [P, i32, i64, i64, P, P, P]
             L.hqq_mxfp4_dequantize.argtypes = [P, P, i64, i64, i32, P, P]
@@ -115,7 +137,9 @@ def lib() -> ctypes.CDLL:
                       "hqq_quantize_meta", "hqq_dequantize_meta", "hqq_quantize_ex_noalloc",
                       "hqq_quantize_batched", "hqq_dequantize_batched", "hqq_linear",
                       "hqq_wait_timeouts", "hqq_mxfp4_quantize", "hqq_mxfp4_dequantize",
-                      "hqq_quantize_mixed", "hqq_dequantize_mixed", "hqq_mixed_plan"):
+                      "hqq_quantize_mixed", "hqq_dequantize_mixed", "hqq_mixed_plan",
+                      "hqq_linear_ex", "hqq_linear_backward", "hqq_gated_linear",
+                      "hqq_gated_linear_backward"):
                 getattr(L, f).restype = i32
             L.hqq_packed_bytes.argtypes = [i64, i64, i32, i32, i32]
             L.hqq_packed_bytes.restype = sz
@@ -513,6 +537,257 @@ def hqq_linear(X: torch.Tensor, Wq_packed: torch.Tensor, scale: torch.Tensor,
                               N, ctypes.byref(params), _cuda(Y, "Y", dev), _stream(stream, dev))
     _check(st, "hqq_linear")
     return Y
+
+
+class QuantizedWeight:
+    """A quantized weight [rows, cols] ready for the products: its tensors, configuration and the
+    C descriptor built from them once (see quantized_weight)."""
+    __slots__ = ("rows", "cols", "device", "dtype", "tensors", "c", "ref")
+
+    def __init__(self, rows, cols, device, dtype, tensors, c):
+        self.rows, self.cols, self.device, self.dtype = rows, cols, device, dtype
+        self.tensors, self.c = tensors, c
+        self.ref = ctypes.pointer(c)
+
+
+def quantized_weight(q, rows: int, cols: int, params: HQQParams, *,
+                     bias: Optional[torch.Tensor] = None) -> QuantizedWeight:
+    """Bundle a quantized weight for hqq_linear_ex and its companions: q is the result of
+    hqq_quantize_ex (a dict), or the (Wq_packed, scale, zero) of hqq_quantize, of W [rows, cols]
+    with `params`; bias [rows] in the activation dtype. Nothing is copied: the tensors stay
+    referenced, and writing to them changes the weight."""
+    if not isinstance(q, dict):
+        q = dict(zip(("Wq_packed", "scale", "zero"), q))
+    pk, sc, zr = q["Wq_packed"], q["scale"], q["zero"]
+    ng = hqq_num_groups(rows, cols, params.group_size, params.axis)
+    if ng < 0:
+        raise HQQError(3, "quantized_weight")
+    dev = pk.device
+    ptr = {"Wq_packed": _cuda(pk, "Wq_packed"), "scale": _cuda(sc, "scale", dev),
+           "zero": _cuda(zr, "zero", dev), "scale_mm": None, "zero_mm": None, "bias": None}
+    if pk.numel() * pk.element_size() < hqq_packed_bytes(rows, cols, params.nbits):
+        raise ValueError("Wq_packed is smaller than the packed codes of [rows, cols]")
+    tensors = [pk, sc, zr]
+    for name, t, quant in (("scale", sc, params.quant_scale), ("zero", zr, params.quant_zero)):
+        want = torch.uint8 if quant else _DT_TORCH.get(params.meta_dtype)
+        if t.dtype != want or t.numel() != ng:
+            raise ValueError(f"{name} must hold {ng} values of {want} for these params")
+        if quant:
+            mm = q.get(name + "_mm")
+            runs = max(hqq_num_meta_groups(ng, params.meta_group_size), 0)
+            if mm is None or mm.dtype != torch.float32 or mm.numel() != 2 * runs:
+                raise ValueError(f"{name}_mm must hold {runs} float32 pairs for these params")
+            ptr[name + "_mm"] = _cuda(mm, name + "_mm", dev)
+            tensors.append(mm)
+    if bias is not None:
+        if bias.numel() != rows or bias.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"bias must hold {rows} values of the activation dtype")
+        ptr["bias"] = _cuda(bias, "bias", dev)
+        tensors.append(bias)
+    c = HQQWeight(ptr["Wq_packed"], ptr["scale"], ptr["zero"], ptr["scale_mm"], ptr["zero_mm"],
+                  ptr["bias"], rows, cols, params)
+    return QuantizedWeight(rows, cols, dev, None if bias is None else bias.dtype, tensors, c)
+
+
+def hqq_linear_workspace_bytes(M: int, w: QuantizedWeight, backward: bool = False) -> int:
+    return _workspace_size(lib().hqq_linear_workspace_bytes(M, w.ref, int(backward)))
+
+
+def hqq_gated_linear_workspace_bytes(M: int, gate: QuantizedWeight, up: QuantizedWeight,
+                                     backward: bool = False) -> int:
+    return _workspace_size(
+        lib().hqq_gated_linear_workspace_bytes(M, gate.ref, up.ref, int(backward)))
+
+
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
+def _workspace_size(n: int) -> int:
+    if n == _NO_SIZE:
+        raise ValueError("invalid weight or token count")
+    return n
+
+
+def _tokens(t: torch.Tensor, name: str, width: int, dev: torch.device) -> int:
+    """Tokens of a contiguous bf16 / fp16 CUDA tensor [..., width] on dev."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dim() < 1 or t.shape[-1] != width:
+        raise ValueError(f"{name} must be [..., {width}], got {list(t.shape)}")
+    if t.device != dev:
+        _same_device(dev, t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    m = 1
+    for d in t.shape[:-1]:
+        m *= d
+    return m
+
+
+class _Launch:
+    """One product call: the weights' device is made current, the stream is looked up, and
+    tensors that the caller did not give are allocated for the stream that writes them. When that
+    is not the caller's current stream, the caching allocator is told of both (record_stream), so
+    that neither an input nor an output is handed out again while the other stream uses it."""
+    __slots__ = ("dev", "stream", "handle", "guards", "caller", "inputs")
+
+    def __init__(self, dev: torch.device, stream, weights, dtype, *inputs):
+        for w in weights:
+            if w.device != dev:
+                raise ValueError(f"the weights are on {dev} and {w.device}")
+            if w.dtype is not None and w.dtype != dtype:
+                raise ValueError(f"bias is {w.dtype}, but the activations are {dtype}")
+        self.dev, self.stream, self.inputs = dev, stream, inputs
+
+    def __enter__(self):
+        dev, stream = self.dev, self.stream
+        self.handle = _stream(stream, dev)
+        self.guards, self.caller = [], None
+        if torch.cuda.current_device() != dev.index:
+            self.guards.append(torch.cuda.device(dev))
+        if stream is not None:
+            current = torch.cuda.current_stream(dev)
+            if current != stream:
+                self.caller = current
+                self.guards.append(torch.cuda.stream(stream))
+                for t in self.inputs:
+                    t.record_stream(stream)
+        for g in self.guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+    def out(self, t: Optional[torch.Tensor], name: str, shape, dtype) -> torch.Tensor:
+        """`t`, checked to be a contiguous tensor of this shape and dtype, or a new one."""
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=self.dev)
+            if self.caller is not None:
+                t.record_stream(self.caller)
+            return t
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+            raise ValueError(f"{name} must be {list(shape)} of {dtype}")
+        _cuda(t, name, self.dev)
+        return t
+
+    def workspace(self, given, need: int):
+        """(pointer, bytes) of the given workspace, or of a new one where some is needed; the
+        third value keeps it alive until the call is enqueued."""
+        if given is not None:
+            return _cuda(given, "workspace", self.dev), given.numel() * given.element_size(), given
+        if need == 0:
+            return None, 0, None
+        t = torch.empty(need, dtype=torch.uint8, device=self.dev)
+        return t.data_ptr(), need, t
+
+
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _act(name: str) -> int:
+    if name not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {name!r}")
+    return _ACTS[name]
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def hqq_linear_ex(X: torch.Tensor, w: QuantizedWeight, *, Y: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Forward pass of a quantized linear layer in any format: Y = X @ W'.T (+ w's bias), X
+    [..., cols] bf16 or fp16. A few tokens are multiplied straight from the packed codes; more
+    take a workspace (hqq_linear_workspace_bytes; allocated here when not given)."""
+    M = _tokens(X, "X", w.cols, w.device)
+    with _Launch(w.device, stream, (w,), X.dtype, X) as run:
+        Y = run.out(Y, "Y", (*X.shape[:-1], w.rows), X.dtype)
+        L = lib()
+        need = L.hqq_linear_workspace_bytes(M, w.ref, 0) if workspace is None else 0
+        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
+        st = L.hqq_linear_ex(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), w.ref, Y.data_ptr(),
+                             wp, wn, run.handle)
+    _check(st, "hqq_linear_ex")
+    return Y
+
+
+def hqq_linear_backward(dY: torch.Tensor, w: QuantizedWeight, *, bias_grad: bool = False,
+                        dX: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of hqq_linear_ex (or hqq_linear) for its input: dX = dY @ W'. With bias_grad (or
+    a dbias to write) returns (dX, dbias), dbias the sum of dY over the tokens."""
+    M = _tokens(dY, "dY", w.rows, w.device)
+    with _Launch(w.device, stream, (w,), dY.dtype, dY) as run:
+        dX = run.out(dX, "dX", (*dY.shape[:-1], w.cols), dY.dtype)
+        if bias_grad or dbias is not None:
+            dbias = run.out(dbias, "dbias", (w.rows,), dY.dtype)
+        L = lib()
+        need = L.hqq_linear_workspace_bytes(M, w.ref, 1) if workspace is None else 0
+        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
+        st = L.hqq_linear_backward(dY.data_ptr(), M, _TORCH_DT.get(dY.dtype, -1), w.ref,
+                                   dX.data_ptr(), _ptr(dbias), wp, wn, run.handle)
+    _check(st, "hqq_linear_backward")
+    return dX if dbias is None else (dX, dbias)
+
+
+def hqq_gated_linear(X: torch.Tensor, gate: QuantizedWeight, up: QuantizedWeight,
+                     act: str = "silu", *, save: bool = False, Y: Optional[torch.Tensor] = None,
+                     G: Optional[torch.Tensor] = None, U: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """The gated pair of projections of a feed-forward block: Y = act(X @ Wg'.T (+ bias)) *
+    (X @ Wu'.T (+ bias)), act "silu", "gelu" or "gelu_tanh". With save (or G and U to write)
+    returns (Y, G, U), the projections that hqq_gated_linear_backward needs."""
+    code = _act(act)
+    M = _tokens(X, "X", gate.cols, gate.device)
+    with _Launch(gate.device, stream, (gate, up), X.dtype, X) as run:
+        shape = (*X.shape[:-1], gate.rows)
+        Y = run.out(Y, "Y", shape, X.dtype)
+        if save or G is not None or U is not None:
+            G = run.out(G, "G", shape, X.dtype)
+            U = run.out(U, "U", shape, X.dtype)
+        L = lib()
+        need = L.hqq_gated_linear_workspace_bytes(M, gate.ref, up.ref, 0) \
+            if workspace is None else 0
+        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
+        st = L.hqq_gated_linear(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), gate.ref, up.ref,
+                                code, Y.data_ptr(), _ptr(G), _ptr(U), wp, wn, run.handle)
+    _check(st, "hqq_gated_linear")
+    return Y if G is None else (Y, G, U)
+
+
+def hqq_gated_linear_backward(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
+                              gate: QuantizedWeight, up: QuantizedWeight, act: str = "silu", *,
+                              bias_grad: bool = False, dX: Optional[torch.Tensor] = None,
+                              dG: Optional[torch.Tensor] = None,
+                              dU: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of hqq_gated_linear from its saved G and U: returns (dX, dG, dU), and with
+    bias_grad also the sums of dG and dU over the tokens, (dX, dG, dU, dbias_gate, dbias_up)."""
+    code = _act(act)
+    dev = gate.device
+    M = _tokens(dY, "dY", gate.rows, dev)
+    for name, t in (("G", G), ("U", U)):
+        if t.dtype != dY.dtype or t.shape != dY.shape:
+            raise ValueError(f"{name} must be like dY")
+        _cuda(t, name, dev)
+    with _Launch(dev, stream, (gate, up), dY.dtype, dY, G, U) as run:
+        dX = run.out(dX, "dX", (*dY.shape[:-1], gate.cols), dY.dtype)
+        dG = run.out(dG, "dG", dY.shape, dY.dtype)
+        dU = run.out(dU, "dU", dY.shape, dY.dtype)
+        db = [run.out(None, "dbias", (gate.rows,), dY.dtype) if bias_grad else None
+              for _ in range(2)]
+        L = lib()
+        need = L.hqq_gated_linear_workspace_bytes(M, gate.ref, up.ref, 1) \
+            if workspace is None else 0
+        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
+        st = L.hqq_gated_linear_backward(
+            dY.data_ptr(), G.data_ptr(), U.data_ptr(), M, _TORCH_DT.get(dY.dtype, -1), gate.ref,
+            up.ref, code, dG.data_ptr(), dU.data_ptr(), dX.data_ptr(), _ptr(db[0]), _ptr(db[1]),
+            wp, wn, run.handle)
+    _check(st, "hqq_gated_linear_backward")
+    return (dX, dG, dU, *db) if bias_grad else (dX, dG, dU)
 
 
 def hqq_wait_timeouts() -> int:

@@ -18,8 +18,11 @@ ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhqq_b200.so")
 SOURCES = ["hqq_abi.cu", "hqq_quantize.cu", "hqq_quantize_stop.cu", "hqq_dequantize.cu",
-           "hqq_noalloc.cu", "hqq_gemm.cu", "hqq_mx.cu"]
-HEADERS = ["hqq_device.cuh", "hqq_kernels.h", "hqq_quantize_impl.cuh", "hqq_abi_internal.h"]
+           "hqq_noalloc.cu", "hqq_gemm.cu", "hqq_mx.cu", "hqq_abi_product.cu", "hqq_few.cu",
+           "hqq_few_1.cu", "hqq_few_2.cu", "hqq_few_3.cu", "hqq_few_4.cu", "hqq_few_8.cu",
+           "hqq_dense.cu"]
+HEADERS = ["hqq_device.cuh", "hqq_tensor.cuh", "hqq_act.cuh", "hqq_kernels.h",
+           "hqq_quantize_impl.cuh", "hqq_few_impl.cuh", "hqq_abi_internal.h"]
 PUBLIC_HEADER = os.path.join(ROOT, "include", "hqq", "hqq.h")
 
 NVCC_FLAGS = [

@@ -39,7 +39,10 @@ hqq_status hqqabi::check_device(const void* p) {
   return at.device == dev ? HQQ_OK : HQQ_ERR_INVALID_ARG;
 }
 
+using hqqabi::aligned;
 using hqqabi::check_device;
+using hqqabi::check_meta_group;
+using hqqabi::check_shape;
 using hqqabi::cuda_status;
 
 namespace {
@@ -52,10 +55,20 @@ bool nbits_ok(int nbits) {
 bool group_ok(int g) { return g == 8 || g == 16 || g == 32 || g == 64 || g == 128 || g == 256; }
 bool wdtype_ok(int dt) { return dt == HQQ_F16 || dt == HQQ_BF16 || dt == HQQ_F32; }
 size_t dtype_size(int dt) { return dt == HQQ_F32 ? 4 : dt == HQQ_U8 ? 1 : 2; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Shape checks shared by quantize and dequantize.
-hqq_status check_shape(int64_t rows, int64_t cols, int nbits, int group_size, int axis) {
+}  // namespace
+
+bool hqqabi::aligned(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+
+bool hqqabi::float_dtype(int dt) { return wdtype_ok(dt); }
+
+hqq_status hqqabi::check_meta_group(int g) {
+  return (g >= 8 && g <= 1024) ? HQQ_OK : HQQ_ERR_UNSUPPORTED;
+}
+
+hqq_status hqqabi::check_shape(int64_t rows, int64_t cols, int nbits, int group_size, int axis) {
   if (rows < 0 || cols < 0) return HQQ_ERR_INVALID_ARG;
   if (!nbits_ok(nbits) || !group_ok(group_size) || (axis != 0 && axis != 1))
     return HQQ_ERR_UNSUPPORTED;
@@ -64,6 +77,8 @@ hqq_status check_shape(int64_t rows, int64_t cols, int nbits, int group_size, in
   if (axis == 0 && rows % group_size) return HQQ_ERR_SHAPE;
   return HQQ_OK;
 }
+
+namespace {
 
 bool flags_ok(int flags) { return (flags & ~HQQ_FLAG_STOP_AT_FIXED_POINT) == 0; }
 
@@ -74,8 +89,6 @@ hqq_status check_solver(int iters, float p, float beta0, float kappa) {
   if (!(kappa >= 1.0f) || !isfinite(kappa)) return HQQ_ERR_INVALID_ARG;
   return HQQ_OK;
 }
-
-hqq_status check_meta_group(int g) { return (g >= 8 && g <= 1024) ? HQQ_OK : HQQ_ERR_UNSUPPORTED; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -562,7 +575,11 @@ HQQ_EXPORT hqq_status hqq_linear(const void* X, int64_t M, int64_t K, hqq_dtype 
 
 HQQ_EXPORT hqq_status hqq_wait_timeouts(unsigned int* count) {
   if (!count) return HQQ_ERR_INVALID_ARG;
-  return cuda_status(hqqk::read_gemm_timeouts(count));
+  unsigned int gemm = 0, dense = 0;
+  hqq_status st = cuda_status(hqqk::read_gemm_timeouts(&gemm));
+  if (st == HQQ_OK) st = cuda_status(hqqk::read_dense_timeouts(&dense));
+  if (st == HQQ_OK) *count = gemm + dense;
+  return st;
 }
 
 static hqq_status check_mx_shape(int64_t rows, int64_t cols) {

@@ -21,4 +21,12 @@ hqq_status validate_quantize(const void* W, int64_t rows, int64_t cols, const hq
 // host memory the GPU cannot address (neither pinned nor managed); HQQ_OK otherwise.
 hqq_status check_device(const void* p);
 
+// Shape checks shared by every call on a [rows, cols] weight of one configuration.
+hqq_status check_shape(int64_t rows, int64_t cols, int nbits, int group_size, int axis);
+// HQQ_OK for a run length the second level supports.
+hqq_status check_meta_group(int g);
+// F16, BF16 or F32.
+bool float_dtype(int dt);
+bool aligned(const void* p, size_t a);
+
 }  // namespace hqqabi

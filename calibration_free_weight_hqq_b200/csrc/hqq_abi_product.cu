@@ -1,0 +1,322 @@
+// hqq_abi_product.cu - extern "C" entry points of the products over quantized weights (linear
+// layers of every format, the gated pair, their gradients): argument validation, the choice of
+// kernel, and the order of the launches. The contract is in include/hqq/hqq.h.
+#include <algorithm>
+
+#include "../../include/hqq/hqq.h"
+#include "hqq_abi_internal.h"
+#include "hqq_kernels.h"
+
+#define HQQ_EXPORT extern "C" __attribute__((visibility("default")))
+
+static_assert((int)HQQ_ACT_SILU == hqqk::kSilu && (int)HQQ_ACT_GELU == hqqk::kGelu &&
+                  (int)HQQ_ACT_GELU_TANH == hqqk::kGeluTanh,
+              "activation enumerators must match");
+
+using hqqabi::aligned;
+using hqqabi::check_device;
+using hqqabi::cuda_status;
+
+namespace {
+
+// Tokens up to which the few-token kernel serves a product (see use_few).
+constexpr int64_t kFewMaxTokens = 32;
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;
+
+size_t weight_bytes(const hqq_weight& w) {  // the dequantized weight, 256-byte aligned
+  return (static_cast<size_t>(w.rows) * static_cast<size_t>(w.cols) * 2 + 255) / 256 * 256;
+}
+
+// Everything about a weight that needs no token count: configuration, shape, pointers.
+hqq_status check_weight(const hqq_weight* w) {
+  if (!w) return HQQ_ERR_INVALID_ARG;
+  const hqq_params& p = w->params;
+  hqq_status st = hqqabi::check_shape(w->rows, w->cols, p.nbits, p.group_size, p.axis);
+  if (st != HQQ_OK) return st;
+  const bool qs = p.quant_scale != 0, qz = p.quant_zero != 0;
+  if (!hqqabi::float_dtype(p.meta_dtype)) return HQQ_ERR_UNSUPPORTED;
+  if ((qs || qz) && (st = hqqabi::check_meta_group(p.meta_group_size)) != HQQ_OK) return st;
+  if ((p.flags & ~(HQQ_FLAG_STOP_AT_FIXED_POINT | HQQ_FLAG_OVERLAP_WEIGHTS)) != 0)
+    return HQQ_ERR_INVALID_ARG;
+  if (w->rows % 8 != 0 || w->cols % 8 != 0 || w->rows >= kMaxDim || w->cols >= kMaxDim)
+    return HQQ_ERR_SHAPE;
+  if (!aligned(w->bias, 2)) return HQQ_ERR_ALIGNMENT;
+  if (w->rows * w->cols == 0) return HQQ_OK;
+  if (!w->Wq_packed || !w->scale || !w->zero) return HQQ_ERR_INVALID_ARG;
+  if ((qs && !w->scale_mm) || (qz && !w->zero_mm)) return HQQ_ERR_INVALID_ARG;
+  const size_t msz = p.meta_dtype == HQQ_F32 ? 4 : 2;
+  if (!aligned(w->Wq_packed, 16) || (!qs && !aligned(w->scale, msz)) ||
+      (!qz && !aligned(w->zero, msz)) || (qs && !aligned(w->scale_mm, 8)) ||
+      (qz && !aligned(w->zero_mm, 8)))
+    return HQQ_ERR_ALIGNMENT;
+  return HQQ_OK;
+}
+
+hqq_status check_pair(const hqq_weight* gate, const hqq_weight* up) {
+  hqq_status st = check_weight(gate);
+  if (st != HQQ_OK || (st = check_weight(up)) != HQQ_OK) return st;
+  return gate->rows == up->rows && gate->cols == up->cols ? HQQ_OK : HQQ_ERR_SHAPE;
+}
+
+hqq_status check_tokens(int64_t M, int dtype) {
+  if (M < 0) return HQQ_ERR_INVALID_ARG;
+  if (dtype != HQQ_BF16 && dtype != HQQ_F16) return HQQ_ERR_UNSUPPORTED;
+  return M < kMaxDim ? HQQ_OK : HQQ_ERR_SHAPE;
+}
+
+bool act_ok(int act) {
+  return act == HQQ_ACT_SILU || act == HQQ_ACT_GELU || act == HQQ_ACT_GELU_TANH;
+}
+
+// The formats agree in everything the few-token kernel reads.
+bool same_format(const hqq_params& a, const hqq_params& b) {
+  return a.nbits == b.nbits && a.group_size == b.group_size && a.axis == b.axis &&
+         a.meta_dtype == b.meta_dtype && !a.quant_scale == !b.quant_scale &&
+         !a.quant_zero == !b.quant_zero &&
+         ((!a.quant_scale && !a.quant_zero) || a.meta_group_size == b.meta_group_size);
+}
+
+// Whether a forward product runs on the few-token kernel: groups along the rows, one format,
+// few tokens. A weight of no columns has an empty sum in either kernel; that one writes it.
+bool use_few(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  if (w.cols == 0) return true;
+  if (M > kFewMaxTokens || w.params.axis != 1) return false;
+  return up == nullptr || same_format(w.params, up->params);
+}
+
+size_t forward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  if (M == 0 || use_few(M, w, up)) return 0;
+  return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
+}
+
+size_t backward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  if (M == 0) return 0;
+  return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
+}
+
+hqqk::WeightView view(const hqq_weight& w) {
+  hqqk::WeightView v;
+  v.packed = static_cast<const uint8_t*>(w.Wq_packed);
+  v.scale = w.scale;
+  v.zero = w.zero;
+  v.scale_mm = w.params.quant_scale ? static_cast<const float*>(w.scale_mm) : nullptr;
+  v.zero_mm = w.params.quant_zero ? static_cast<const float*>(w.zero_mm) : nullptr;
+  v.bias = w.bias;
+  return v;
+}
+
+hqqk::DequantJob dequant_job(const hqq_weight& w, int dtype, void* out) {
+  const hqqk::WeightView v = view(w);
+  hqqk::DequantJob j;
+  j.packed = v.packed;
+  j.scale = v.scale;
+  j.zero = v.zero;
+  j.scale_mm = v.scale_mm;
+  j.zero_mm = v.zero_mm;
+  j.meta_group_size = w.params.meta_group_size;
+  j.meta_dtype = w.params.meta_dtype;
+  j.rows = w.rows;
+  j.cols = w.cols;
+  j.n_groups = w.rows * w.cols / w.params.group_size;
+  j.nbits = w.params.nbits;
+  j.group_size = w.params.group_size;
+  j.axis = w.params.axis;
+  j.out_dtype = dtype;
+  j.out = out;
+  return j;
+}
+
+// The weight, or both of a pair, dequantized into the workspace, one after the other: W'[i] in
+// out[i].
+hqq_status dequantize_into(void* workspace, const hqq_weight& w, const hqq_weight* up, int dtype,
+                           const void* (&out)[2], cudaStream_t stream) {
+  out[0] = workspace;
+  out[1] = static_cast<char*>(workspace) + (up ? weight_bytes(w) : 0);
+  hqq_status st = cuda_status(
+      hqqk::launch_dequantize(dequant_job(w, dtype, const_cast<void*>(out[0])), stream));
+  if (st == HQQ_OK && up)
+    st = cuda_status(
+        hqqk::launch_dequantize(dequant_job(*up, dtype, const_cast<void*>(out[1])), stream));
+  return st;
+}
+
+hqq_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return HQQ_OK;
+  if (!workspace || bytes < need) return HQQ_ERR_WORKSPACE;
+  return aligned(workspace, 16) ? HQQ_OK : HQQ_ERR_ALIGNMENT;
+}
+
+// The few-token kernel over any number of tokens (its grid holds 65535 tiles of them).
+hqq_status run_few(hqqk::FewJob j, cudaStream_t stream) {
+  constexpr int64_t kChunk = 65535 * 8;
+  const int64_t M = j.M;
+  auto at = [](void* p, int64_t elems) {
+    return p == nullptr ? nullptr : static_cast<void*>(static_cast<char*>(p) + 2 * elems);
+  };
+  const hqqk::FewJob whole = j;
+  for (int64_t m = 0; m < M; m += kChunk) {
+    j.M = std::min<int64_t>(kChunk, M - m);
+    j.X = static_cast<const char*>(whole.X) + 2 * m * j.K;
+    j.Y = at(whole.Y, m * j.N);
+    j.G = at(whole.G, m * j.N);
+    j.U = at(whole.U, m * j.N);
+    const hqq_status st = cuda_status(hqqk::launch_few(j, stream));
+    if (st != HQQ_OK) return st;
+  }
+  return HQQ_OK;
+}
+
+hqq_status forward(const void* X, int64_t M, int dtype, const hqq_weight& w, const hqq_weight* up,
+                   int act, void* Y, void* G, void* U, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+  if (M == 0 || w.rows == 0) return HQQ_OK;
+  if (!Y || (w.cols > 0 && !X)) return HQQ_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(G, 16) || !aligned(U, 16))
+    return HQQ_ERR_ALIGNMENT;
+  hqq_status st = check_workspace(workspace, workspace_bytes, forward_need(M, w, up));
+  if (st != HQQ_OK) return st;
+  if ((st = check_device(w.cols > 0 ? X : Y)) != HQQ_OK) return st;
+  if (use_few(M, w, up)) {
+    hqqk::FewJob j = {};
+    j.X = X;
+    j.w[0] = view(w);
+    if (up) j.w[1] = view(*up);
+    j.mats = up ? 2 : 1;
+    j.M = M;
+    j.N = w.rows;
+    j.K = w.cols;
+    j.x_dtype = dtype;
+    j.nbits = w.params.nbits;
+    j.group_size = w.params.group_size;
+    j.meta_dtype = w.params.meta_dtype;
+    j.meta_group_size = std::max(w.params.meta_group_size, 1);
+    j.act = act;
+    j.Y = Y;
+    j.G = G;
+    j.U = U;
+    return run_few(j, stream);
+  }
+  hqqk::DenseJob j = {};
+  if ((st = dequantize_into(workspace, w, up, dtype, j.B, stream)) != HQQ_OK) return st;
+  j.kind = up ? hqqk::kDenseGated : hqqk::kDenseForward;
+  j.A[0] = X;
+  j.bias[0] = w.bias;
+  j.bias[1] = up ? up->bias : nullptr;
+  j.sources = 1;
+  j.M = M;
+  j.N = w.rows;
+  j.K = w.cols;
+  j.x_dtype = dtype;
+  j.act = act;
+  j.D = Y;
+  j.G = G;
+  j.U = U;
+  return cuda_status(hqqk::launch_dense(j, stream));
+}
+
+// dX[M, cols] = sum over the weights of A[i][M, rows] W'[i].
+hqq_status backward(const void* const (&A)[2], int64_t M, int dtype, const hqq_weight& w,
+                    const hqq_weight* up, void* dX, void* workspace, cudaStream_t stream) {
+  if (M == 0 || w.cols == 0) return HQQ_OK;
+  if (w.rows == 0)  // an empty sum
+    return cuda_status(cudaMemsetAsync(dX, 0, static_cast<size_t>(M) * w.cols * 2, stream));
+  hqqk::DenseJob j = {};
+  const hqq_status st = dequantize_into(workspace, w, up, dtype, j.B, stream);
+  if (st != HQQ_OK) return st;
+  j.kind = hqqk::kDenseBackward;
+  j.A[0] = A[0];
+  j.A[1] = A[1];
+  j.sources = up ? 2 : 1;
+  j.M = M;
+  j.N = w.cols;
+  j.K = w.rows;
+  j.x_dtype = dtype;
+  j.D = dX;
+  return cuda_status(hqqk::launch_dense(j, stream));
+}
+
+}  // namespace
+
+HQQ_EXPORT size_t hqq_linear_workspace_bytes(int64_t M, const hqq_weight* w, int backward_pass) {
+  if (M < 0 || M >= kMaxDim || check_weight(w) != HQQ_OK) return static_cast<size_t>(-1);
+  return backward_pass ? backward_need(M, *w, nullptr) : forward_need(M, *w, nullptr);
+}
+
+HQQ_EXPORT size_t hqq_gated_linear_workspace_bytes(int64_t M, const hqq_weight* gate,
+                                                   const hqq_weight* up, int backward_pass) {
+  if (M < 0 || M >= kMaxDim || check_pair(gate, up) != HQQ_OK) return static_cast<size_t>(-1);
+  return backward_pass ? backward_need(M, *gate, up) : forward_need(M, *gate, up);
+}
+
+HQQ_EXPORT hqq_status hqq_linear_ex(const void* X, int64_t M, hqq_dtype x_dtype,
+                                    const hqq_weight* w, void* Y, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  hqq_status st = check_weight(w);
+  if (st != HQQ_OK || (st = check_tokens(M, x_dtype)) != HQQ_OK) return st;
+  return forward(X, M, x_dtype, *w, nullptr, HQQ_ACT_SILU, Y, nullptr, nullptr, workspace,
+                 workspace_bytes, stream);
+}
+
+HQQ_EXPORT hqq_status hqq_gated_linear(const void* X, int64_t M, hqq_dtype x_dtype,
+                                       const hqq_weight* gate, const hqq_weight* up, hqq_act act,
+                                       void* Y, void* G, void* U, void* workspace,
+                                       size_t workspace_bytes, cudaStream_t stream) {
+  hqq_status st = check_pair(gate, up);
+  if (st != HQQ_OK || (st = check_tokens(M, x_dtype)) != HQQ_OK) return st;
+  if (!act_ok(act)) return HQQ_ERR_UNSUPPORTED;
+  return forward(X, M, x_dtype, *gate, up, act, Y, G, U, workspace, workspace_bytes, stream);
+}
+
+HQQ_EXPORT hqq_status hqq_linear_backward(const void* dY, int64_t M, hqq_dtype x_dtype,
+                                          const hqq_weight* w, void* dX, void* dbias,
+                                          void* workspace, size_t workspace_bytes,
+                                          cudaStream_t stream) {
+  hqq_status st = check_weight(w);
+  if (st != HQQ_OK || (st = check_tokens(M, x_dtype)) != HQQ_OK) return st;
+  const bool product = M > 0 && w->cols > 0, sums = dbias != nullptr && w->rows > 0;
+  if (!product && !sums) return HQQ_OK;
+  if ((product && !dX) || (M > 0 && w->rows > 0 && !dY)) return HQQ_ERR_INVALID_ARG;
+  if (!aligned(dY, 16) || !aligned(dX, 16) || !aligned(dbias, 2)) return HQQ_ERR_ALIGNMENT;
+  st = check_workspace(workspace, workspace_bytes, product ? backward_need(M, *w, nullptr) : 0);
+  if (st != HQQ_OK) return st;
+  if ((st = check_device(dY ? dY : product ? dX : dbias)) != HQQ_OK) return st;
+  const void* A[2] = {dY, nullptr};
+  if ((st = backward(A, M, x_dtype, *w, nullptr, dX, workspace, stream)) != HQQ_OK) return st;
+  if (!sums) return HQQ_OK;
+  return cuda_status(hqqk::launch_column_sum(dY, M, w->rows, x_dtype, dbias, stream));
+}
+
+HQQ_EXPORT hqq_status hqq_gated_linear_backward(const void* dY, const void* G, const void* U,
+                                                int64_t M, hqq_dtype x_dtype,
+                                                const hqq_weight* gate, const hqq_weight* up,
+                                                hqq_act act, void* dG, void* dU, void* dX,
+                                                void* dbias_gate, void* dbias_up, void* workspace,
+                                                size_t workspace_bytes, cudaStream_t stream) {
+  hqq_status st = check_pair(gate, up);
+  if (st != HQQ_OK || (st = check_tokens(M, x_dtype)) != HQQ_OK) return st;
+  if (!act_ok(act)) return HQQ_ERR_UNSUPPORTED;
+  const int64_t N = gate->rows, K = gate->cols;
+  const bool product = M > 0 && K > 0, rows = M > 0 && N > 0;
+  const bool sums = N > 0 && (dbias_gate != nullptr || dbias_up != nullptr);
+  if (!product && !rows && !sums) return HQQ_OK;
+  if ((rows && (!dY || !G || !U || !dG || !dU)) || (product && !dX)) return HQQ_ERR_INVALID_ARG;
+  for (const void* p : {dY, G, U, static_cast<const void*>(dG), static_cast<const void*>(dU),
+                        static_cast<const void*>(dX)})
+    if (!aligned(p, 16)) return HQQ_ERR_ALIGNMENT;
+  if (!aligned(dbias_gate, 2) || !aligned(dbias_up, 2)) return HQQ_ERR_ALIGNMENT;
+  st = check_workspace(workspace, workspace_bytes, product ? backward_need(M, *gate, up) : 0);
+  if (st != HQQ_OK) return st;
+  const void* first = rows ? dY : product ? dX : dbias_gate ? dbias_gate : dbias_up;
+  if ((st = check_device(first)) != HQQ_OK) return st;
+  if (rows)
+    st = cuda_status(hqqk::launch_gated_grad(dY, G, U, M * N, x_dtype, act, dG, dU, stream));
+  if (st != HQQ_OK) return st;
+  const void* A[2] = {dG, dU};
+  if ((st = backward(A, M, x_dtype, *gate, up, dX, workspace, stream)) != HQQ_OK) return st;
+  if (N > 0 && dbias_gate)
+    st = cuda_status(hqqk::launch_column_sum(dG, M, N, x_dtype, dbias_gate, stream));
+  if (st == HQQ_OK && N > 0 && dbias_up)
+    st = cuda_status(hqqk::launch_column_sum(dU, M, N, x_dtype, dbias_up, stream));
+  return st;
+}

@@ -70,6 +70,61 @@ cudaError_t launch_w4a16_gemm(const GemmJob& job, cudaStream_t stream);
 // loaded (0 on every healthy run).
 cudaError_t read_gemm_timeouts(unsigned int* out);
 
+// Activations of the gated products; the values equal the public hqq_act enumerators.
+enum Act : int { kSilu = 0, kGelu = 1, kGeluTanh = 2 };
+
+// A quantized weight [N, K] of a product; bias: nullptr or [N] of the activation dtype.
+struct WeightView {
+  const uint8_t* packed;
+  const void* scale;  // meta_dtype values, or uint8 codes when scale_mm != nullptr
+  const void* zero;
+  const float* scale_mm;
+  const float* zero_mm;
+  const void* bias;
+};
+
+// Few-token product over one weight (mats = 1: Y = X W'^T + bias) or the gated pair (mats = 2:
+// Y = act(X Wg'^T + bg) * (X Wu'^T + bu)); axis 1, any nbits and group size, both weights of
+// one format. G, U: nullptr or where the gated pair's projections go, rounded.
+struct FewJob {
+  const void* X;
+  WeightView w[2];
+  int mats;
+  int64_t M, N, K;
+  int x_dtype;
+  int nbits, group_size, meta_dtype, meta_group_size;
+  int act;
+  void *Y, *G, *U;
+};
+cudaError_t launch_few(const FewJob& job, cudaStream_t stream);
+
+// Large products on dequantized weights (x_dtype, row-major), on the 2-SM tensor-core kernel.
+enum DenseKind : int {
+  kDenseForward = 0,   // D[M, N] = A[0][M, K] B[0][N, K]^T (+ bias[0])
+  kDenseGated = 1,     // D[M, N] = act(A[0] B[0]^T + bias[0]) * (A[0] B[1]^T + bias[1]); G, U
+  kDenseBackward = 2,  // D[M, N] = sum over i < sources of A[i][M, K] B[i][K, N]
+};
+struct DenseJob {
+  int kind;
+  const void* A[2];
+  const void* B[2];
+  const void* bias[2];
+  int sources;  // of kDenseBackward: 1 or 2
+  int64_t M, N, K;
+  int x_dtype;
+  int act;
+  void *D, *G, *U;
+};
+cudaError_t launch_dense(const DenseJob& job, cudaStream_t stream);
+cudaError_t read_dense_timeouts(unsigned int* out);
+
+// dG = dY * U * act'(G), dU = dY * act(G), elementwise over n values of x_dtype.
+cudaError_t launch_gated_grad(const void* dY, const void* G, const void* U, int64_t n, int x_dtype,
+                              int act, void* dG, void* dU, cudaStream_t stream);
+// out[c] = sum over rows of A[rows, cols], fp32 in a fixed order, rounded once.
+cudaError_t launch_column_sum(const void* A, int64_t rows, int64_t cols, int x_dtype, void* out,
+                              cudaStream_t stream);
+
 // MXFP4: n = rows*cols elements (n % 32 == 0), blocks of 32 consecutive elements.
 cudaError_t launch_mxfp4_quantize(const void* W, int dtype, int64_t n, uint8_t* codes,
                                   uint8_t* scales, cudaStream_t stream);

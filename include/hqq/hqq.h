@@ -330,6 +330,92 @@ hqq_status hqq_linear(const void* X, int64_t M, int64_t K, hqq_dtype x_dtype,
                       const void* bias, int64_t N, const hqq_params* params, void* Y,
                       cudaStream_t stream);
 
+/* ---- Products over quantized weights of every format, and their gradients ----------------
+ *
+ * hqq_linear above is the 4-bit, group-64, axis-1 layer without a workspace; the calls below
+ * take a weight in any format the quantizer writes and add the gradient and the gated pair of
+ * projections of a feed-forward block. Throughout, W' is the weight exactly as hqq_dequantize_ex
+ * writes it in the activation dtype (one rounding per element), products are summed in fp32 in
+ * an unspecified but fixed order (the same call gives the same bits), and each output is
+ * rounded once. The quantized weight itself has no gradient: it stays frozen. */
+
+/* One quantized weight [rows = N output features, cols = K input features] as hqq_quantize* wrote
+ * it. params: the configuration (nbits, group_size, axis, meta_dtype, quant_scale, quant_zero,
+ * meta_group_size; the solver's fields and w_dtype are ignored; flags as in hqq_linear, ignored).
+ *   Wq_packed  device, 16-byte aligned.
+ *   scale, zero, scale_mm, zero_mm
+ *              device, as in hqq_dequantize_ex (the mm pairs only where quantized).
+ *   bias       NULL or device [rows] of the call's activation dtype. */
+typedef struct {
+  const void* Wq_packed;
+  const void* scale;
+  const void* zero;
+  const void* scale_mm;
+  const void* zero_mm;
+  const void* bias;
+  int64_t rows, cols;
+  hqq_params params;
+} hqq_weight;
+
+/* silu: x / (1 + exp(-x)); gelu: x Phi(x) with the normal distribution function Phi; gelu, tanh
+ * form: x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2. */
+typedef enum { HQQ_ACT_SILU = 0, HQQ_ACT_GELU = 1, HQQ_ACT_GELU_TANH = 2 } hqq_act;
+
+/* Rules common to the four calls below.
+ *   M          tokens (0 <= M < 2^31); a call with M == 0 writes nothing but empty sums (zero
+ *              bias gradients).
+ *   shapes     rows % 8 == 0 and cols % 8 == 0 (HQQ_ERR_SHAPE otherwise); gate and up have the
+ *              same shape, their formats may differ.
+ *   x_dtype    HQQ_BF16 or HQQ_F16: every activation, gradient and bias of the call.
+ *   tensors    device, row-major and dense; activations and gradients 16-byte aligned, biases and
+ *              their gradients 2-byte. Outputs must not overlap inputs, the workspace or each
+ *              other.
+ *   workspace  device, 16-byte aligned, at least the bytes the matching *_workspace_bytes call
+ *              returns (NULL is fine when that is 0: a few tokens on an axis-1 weight). It holds
+ *              dequantized weights during the call; its contents before do not matter and after
+ *              are undefined. Two calls that use one workspace at the same time race, captured
+ *              graphs that are replayed concurrently included.
+ * The calls allocate and synchronise nothing and may be captured into a graph. */
+
+/* Workspace of hqq_linear_ex (backward_pass == 0) or hqq_linear_backward (!= 0) for M tokens.
+ * Host only. Returns (size_t)-1 for an invalid weight or M. */
+size_t hqq_linear_workspace_bytes(int64_t M, const hqq_weight* w, int backward_pass);
+
+/* The same of hqq_gated_linear and hqq_gated_linear_backward. */
+size_t hqq_gated_linear_workspace_bytes(int64_t M, const hqq_weight* gate, const hqq_weight* up,
+                                        int backward_pass);
+
+/* Y[M, rows] = dt( X[M, cols] W'^T (+ bias) ). ("HQQ calibration-free guide" (lnwmold.com) §3.2,
+ * HQQLinear forward, for every nbits, group_size and axis of §2.2.) */
+hqq_status hqq_linear_ex(const void* X, int64_t M, hqq_dtype x_dtype, const hqq_weight* w, void* Y,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The gradient of hqq_linear_ex (and of hqq_linear) for dY[M, rows]:
+ * dX[M, cols] = dt( dY W' ); dbias[rows] = dt( sum over tokens of dY ), skipped where NULL. */
+hqq_status hqq_linear_backward(const void* dY, int64_t M, hqq_dtype x_dtype, const hqq_weight* w,
+                               void* dX, void* dbias, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/* The gated pair of projections of a feed-forward block:
+ *   g = X Wg'^T (+ bias), u = X Wu'^T (+ bias), both fp32 and unrounded; Y[M, rows] =
+ *   dt( act(g) * u ).
+ * G, U (each NULL or device [M, rows]) receive g and u rounded to dt: what
+ * hqq_gated_linear_backward needs. */
+hqq_status hqq_gated_linear(const void* X, int64_t M, hqq_dtype x_dtype, const hqq_weight* gate,
+                            const hqq_weight* up, hqq_act act, void* Y, void* G, void* U,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The gradient of hqq_gated_linear for dY[M, rows], from the saved G and U:
+ *   dG = dt( dY * U * act'(G) ), dU = dt( dY * act(G) )  (both outputs: the gradients that
+ *   adapters beside the two projections need), dX[M, cols] = dt( dG Wg' + dU Wu' ) of the
+ *   dG and dU written; dbias_gate, dbias_up [rows] = dt( column sums of dG, dU ), each skipped
+ *   where NULL. */
+hqq_status hqq_gated_linear_backward(const void* dY, const void* G, const void* U, int64_t M,
+                                     hqq_dtype x_dtype, const hqq_weight* gate,
+                                     const hqq_weight* up, hqq_act act, void* dG, void* dU,
+                                     void* dX, void* dbias_gate, void* dbias_up, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream);
+
 /* MXFP4 weight-only encoding ("HQQ calibration-free guide" (lnwmold.com) §5.1 lists an
  * mxfp4 weight-only mode; the encoding is the Open Compute Project Microscaling format
  * MXFP4). W: device, row-major [rows, cols] of dtype (F16, BF16 or F32), 16-byte aligned,
@@ -349,8 +435,8 @@ hqq_status hqq_mxfp4_dequantize(const void* codes, const void* scales, int64_t r
                                 int64_t cols, hqq_dtype out_dtype, void* W_out,
                                 cudaStream_t stream);
 
-/* Kernels that wait on barriers inside a CTA (hqq_linear) bound each wait by about two
- * seconds; a wait that runs out sets the CTA's outputs aside (not written), frees its
+/* Kernels that wait on barriers inside a CTA (hqq_linear, and the products above when they run
+ * on dequantized weights) bound each wait by about two seconds; a wait that runs out sets the CTA's outputs aside (not written), frees its
  * resources and is counted. *count receives the number counted since the library was
  * loaded on the current device (0 on every healthy run). Synchronises the device. */
 hqq_status hqq_wait_timeouts(unsigned int* count);
