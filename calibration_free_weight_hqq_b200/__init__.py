@@ -18,6 +18,7 @@ Parameters mirror BaseQuantizeConfig(nbits, group_size, quant_zero, quant_scale,
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional
@@ -120,7 +121,7 @@ def lib() -> ctypes.CDLL:
             L.hqq_dequantize_meta.argtypes = [P, P, i64, i32, P, P]
             L.hqq_linear.argtypes = [P, i64, i64, i32, P, P, P, P, i64,
                                      ctypes.POINTER(HQQParams), P, P]
-            W = ctypes.POINTER(HQQWeight)
+            W = P  # addresses of HQQWeight structs (QuantizedWeight.ptr)
             L.hqq_linear_workspace_bytes.argtypes = [i64, W, i32]
             L.hqq_gated_linear_workspace_bytes.argtypes = [i64, W, W, i32]
             L.hqq_linear_ex.argtypes = [P, i64, i32, W, P, P, sz, P]
@@ -542,12 +543,13 @@ def hqq_linear(X: torch.Tensor, Wq_packed: torch.Tensor, scale: torch.Tensor,
 class QuantizedWeight:
     """A quantized weight [rows, cols] ready for the products: its tensors, configuration and the
     C descriptor built from them once (see quantized_weight)."""
-    __slots__ = ("rows", "cols", "device", "dtype", "tensors", "c", "ref")
+    __slots__ = ("rows", "cols", "device", "index", "dtype", "tensors", "c", "ptr")
 
     def __init__(self, rows, cols, device, dtype, tensors, c):
-        self.rows, self.cols, self.device, self.dtype = rows, cols, device, dtype
+        self.rows, self.cols, self.device, self.index = rows, cols, device, device.index
+        self.dtype = dtype        # of the bias: the activations' (None without one)
         self.tensors, self.c = tensors, c
-        self.ref = ctypes.pointer(c)
+        self.ptr = ctypes.addressof(c)
 
 
 def quantized_weight(q, rows: int, cols: int, params: HQQParams, *,
@@ -590,97 +592,117 @@ def quantized_weight(q, rows: int, cols: int, params: HQQParams, *,
 
 
 def hqq_linear_workspace_bytes(M: int, w: QuantizedWeight, backward: bool = False) -> int:
-    return _workspace_size(lib().hqq_linear_workspace_bytes(M, w.ref, int(backward)))
+    return _size(lib().hqq_linear_workspace_bytes(M, w.ptr, int(backward)))
 
 
 def hqq_gated_linear_workspace_bytes(M: int, gate: QuantizedWeight, up: QuantizedWeight,
                                      backward: bool = False) -> int:
-    return _workspace_size(
-        lib().hqq_gated_linear_workspace_bytes(M, gate.ref, up.ref, int(backward)))
+    return _size(lib().hqq_gated_linear_workspace_bytes(M, gate.ptr, up.ptr, int(backward)))
 
 
 _NO_SIZE = ctypes.c_size_t(-1).value
 
 
-def _workspace_size(n: int) -> int:
+def _size(n: int) -> int:
     if n == _NO_SIZE:
         raise ValueError("invalid weight or token count")
     return n
 
 
-def _tokens(t: torch.Tensor, name: str, width: int, dev: torch.device) -> int:
-    """Tokens of a contiguous bf16 / fp16 CUDA tensor [..., width] on dev."""
+def _tokens(t: torch.Tensor, name: str, width: int, w: QuantizedWeight) -> int:
+    """Tokens of a contiguous CUDA tensor [..., width] on w's device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dim() < 1 or t.shape[-1] != width:
-        raise ValueError(f"{name} must be [..., {width}], got {list(t.shape)}")
-    if t.device != dev:
-        _same_device(dev, t, name)
+    shape = t.shape
+    if not len(shape) or shape[-1] != width:
+        raise ValueError(f"{name} must be [..., {width}], got {list(shape)}")
+    if t.get_device() != w.index:
+        _same_device(w.device, t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    m = 1
-    for d in t.shape[:-1]:
-        m *= d
-    return m
+    return t.numel() // width if width else math.prod(shape[:-1])
 
 
-class _Launch:
-    """One product call: the weights' device is made current, the stream is looked up, and
-    tensors that the caller did not give are allocated for the stream that writes them. When that
-    is not the caller's current stream, the caching allocator is told of both (record_stream), so
-    that neither an input nor an output is handed out again while the other stream uses it."""
-    __slots__ = ("dev", "stream", "handle", "guards", "caller", "inputs")
+def _check_weights(dtype: torch.dtype, w: QuantizedWeight, up: Optional[QuantizedWeight] = None):
+    for v in (w,) if up is None else (w, up):
+        if v.dtype is not None and v.dtype != dtype:
+            raise ValueError(f"bias is {v.dtype}, but the activations are {dtype}")
+    if up is not None and up.index != w.index:
+        raise ValueError(f"the weights are on {w.device} and {up.device}")
 
-    def __init__(self, dev: torch.device, stream, weights, dtype, *inputs):
-        for w in weights:
-            if w.device != dev:
-                raise ValueError(f"the weights are on {dev} and {w.device}")
-            if w.dtype is not None and w.dtype != dtype:
-                raise ValueError(f"bias is {w.dtype}, but the activations are {dtype}")
-        self.dev, self.stream, self.inputs = dev, stream, inputs
 
-    def __enter__(self):
-        dev, stream = self.dev, self.stream
-        self.handle = _stream(stream, dev)
-        self.guards, self.caller = [], None
-        if torch.cuda.current_device() != dev.index:
-            self.guards.append(torch.cuda.device(dev))
-        if stream is not None:
-            current = torch.cuda.current_stream(dev)
-            if current != stream:
-                self.caller = current
-                self.guards.append(torch.cuda.stream(stream))
-                for t in self.inputs:
-                    t.record_stream(stream)
+class _OnStream:
+    """A product call on a device or stream that is not the current one. Within it new tensors come
+    from that stream's memory, and the caching allocator is told (record_stream) of inputs used there
+    and of outputs the caller's stream will use, so that neither is handed out again too early."""
+
+    def __init__(self, w: QuantizedWeight, stream, inputs):
+        self.caller = torch.cuda.current_stream(w.device)
+        self.handle = _stream(stream, w.device)
+        self.guards = [torch.cuda.device(w.device)]
+        self.other = stream is not None and stream != self.caller
+        if self.other:
+            self.guards.append(torch.cuda.stream(stream))
+            for t in inputs:
+                t.record_stream(stream)
         for g in self.guards:
             g.__enter__()
-        return self
 
-    def __exit__(self, *exc):
+    def leave(self, *outputs):
         for g in reversed(self.guards):
-            g.__exit__(*exc)
+            g.__exit__(None, None, None)
+        if self.other:
+            for t in outputs:
+                if t is not None:
+                    t.record_stream(self.caller)
 
-    def out(self, t: Optional[torch.Tensor], name: str, shape, dtype) -> torch.Tensor:
-        """`t`, checked to be a contiguous tensor of this shape and dtype, or a new one."""
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=self.dev)
-            if self.caller is not None:
-                t.record_stream(self.caller)
-            return t
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-            raise ValueError(f"{name} must be {list(shape)} of {dtype}")
-        _cuda(t, name, self.dev)
-        return t
 
-    def workspace(self, given, need: int):
-        """(pointer, bytes) of the given workspace, or of a new one where some is needed; the
-        third value keeps it alive until the call is enqueued."""
-        if given is not None:
-            return _cuda(given, "workspace", self.dev), given.numel() * given.element_size(), given
-        if need == 0:
-            return None, 0, None
-        t = torch.empty(need, dtype=torch.uint8, device=self.dev)
-        return t.data_ptr(), need, t
+# The handle of a device's current stream; building a torch.cuda.Stream around it first takes 3 us,
+# a quarter of a one-token call.
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _begin(w: QuantizedWeight, stream, *inputs):
+    """(stream handle, None) where the call runs on the current device and stream, else (handle, an
+    _OnStream to leave when the call is enqueued)."""
+    if stream is None and torch.cuda.current_device() == w.index:
+        return _current_raw_stream(w.index), None
+    on = _OnStream(w, stream, inputs)
+    return on.handle, on
+
+
+def _shape(t: torch.Tensor, width: int):
+    """t's shape with its last dimension replaced."""
+    return (t.shape[0], width) if t.dim() == 2 else t.shape[:-1] + (width,)
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> torch.Tensor:
+    """`t`, checked to be a contiguous tensor of this shape with the dtype and device of `like`, or a
+    new one."""
+    if t is None:
+        return like.new_empty(shape)
+    if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {like.dtype}")
+    _cuda(t, name, like.device)
+    return t
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, w: QuantizedWeight):
+    """The given workspace, a new one, or None where none is needed (or the C call will refuse)."""
+    if given is not None:
+        _cuda(given, "workspace", w.device)
+        return given
+    if need == 0 or need == _NO_SIZE:
+        return None
+    return torch.empty(need, dtype=torch.uint8, device=w.device)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
@@ -692,24 +714,26 @@ def _act(name: str) -> int:
     return _ACTS[name]
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
 def hqq_linear_ex(X: torch.Tensor, w: QuantizedWeight, *, Y: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Forward pass of a quantized linear layer in any format: Y = X @ W'.T (+ w's bias), X
     [..., cols] bf16 or fp16. A few tokens are multiplied straight from the packed codes; more
     take a workspace (hqq_linear_workspace_bytes; allocated here when not given)."""
-    M = _tokens(X, "X", w.cols, w.device)
-    with _Launch(w.device, stream, (w,), X.dtype, X) as run:
-        Y = run.out(Y, "Y", (*X.shape[:-1], w.rows), X.dtype)
-        L = lib()
-        need = L.hqq_linear_workspace_bytes(M, w.ref, 0) if workspace is None else 0
-        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
-        st = L.hqq_linear_ex(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), w.ref, Y.data_ptr(),
-                             wp, wn, run.handle)
-    _check(st, "hqq_linear_ex")
+    M = _tokens(X, "X", w.cols, w)
+    if w.dtype is not None:
+        _check_weights(X.dtype, w)
+    L = _lib or lib()
+    handle, on = _begin(w, stream, X)
+    try:
+        Y = _out(Y, "Y", _shape(X, w.rows), X)
+        ws = _workspace(workspace, L.hqq_linear_workspace_bytes(M, w.ptr, 0), w)
+        st = L.hqq_linear_ex(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), w.ptr, Y.data_ptr(),
+                             _ptr(ws), _nbytes(ws), handle)
+    finally:
+        if on is not None:
+            on.leave(Y)
+    if st:
+        _check(st, "hqq_linear_ex")
     return Y
 
 
@@ -718,17 +742,21 @@ def hqq_linear_backward(dY: torch.Tensor, w: QuantizedWeight, *, bias_grad: bool
                         workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradient of hqq_linear_ex (or hqq_linear) for its input: dX = dY @ W'. With bias_grad (or
     a dbias to write) returns (dX, dbias), dbias the sum of dY over the tokens."""
-    M = _tokens(dY, "dY", w.rows, w.device)
-    with _Launch(w.device, stream, (w,), dY.dtype, dY) as run:
-        dX = run.out(dX, "dX", (*dY.shape[:-1], w.cols), dY.dtype)
+    M = _tokens(dY, "dY", w.rows, w)
+    L = _lib or lib()
+    handle, on = _begin(w, stream, dY)
+    try:
+        dX = _out(dX, "dX", _shape(dY, w.cols), dY)
         if bias_grad or dbias is not None:
-            dbias = run.out(dbias, "dbias", (w.rows,), dY.dtype)
-        L = lib()
-        need = L.hqq_linear_workspace_bytes(M, w.ref, 1) if workspace is None else 0
-        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
-        st = L.hqq_linear_backward(dY.data_ptr(), M, _TORCH_DT.get(dY.dtype, -1), w.ref,
-                                   dX.data_ptr(), _ptr(dbias), wp, wn, run.handle)
-    _check(st, "hqq_linear_backward")
+            dbias = _out(dbias, "dbias", (w.rows,), dY)
+        ws = _workspace(workspace, L.hqq_linear_workspace_bytes(M, w.ptr, 1), w)
+        st = L.hqq_linear_backward(dY.data_ptr(), M, _TORCH_DT.get(dY.dtype, -1), w.ptr,
+                                   dX.data_ptr(), _ptr(dbias), _ptr(ws), _nbytes(ws), handle)
+    finally:
+        if on is not None:
+            on.leave(dX, dbias)
+    if st:
+        _check(st, "hqq_linear_backward")
     return dX if dbias is None else (dX, dbias)
 
 
@@ -740,20 +768,25 @@ def hqq_gated_linear(X: torch.Tensor, gate: QuantizedWeight, up: QuantizedWeight
     (X @ Wu'.T (+ bias)), act "silu", "gelu" or "gelu_tanh". With save (or G and U to write)
     returns (Y, G, U), the projections that hqq_gated_linear_backward needs."""
     code = _act(act)
-    M = _tokens(X, "X", gate.cols, gate.device)
-    with _Launch(gate.device, stream, (gate, up), X.dtype, X) as run:
-        shape = (*X.shape[:-1], gate.rows)
-        Y = run.out(Y, "Y", shape, X.dtype)
+    M = _tokens(X, "X", gate.cols, gate)
+    _check_weights(X.dtype, gate, up)
+    L = _lib or lib()
+    handle, on = _begin(gate, stream, X)
+    try:
+        shape = _shape(X, gate.rows)
+        Y = _out(Y, "Y", shape, X)
         if save or G is not None or U is not None:
-            G = run.out(G, "G", shape, X.dtype)
-            U = run.out(U, "U", shape, X.dtype)
-        L = lib()
-        need = L.hqq_gated_linear_workspace_bytes(M, gate.ref, up.ref, 0) \
-            if workspace is None else 0
-        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
-        st = L.hqq_gated_linear(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), gate.ref, up.ref,
-                                code, Y.data_ptr(), _ptr(G), _ptr(U), wp, wn, run.handle)
-    _check(st, "hqq_gated_linear")
+            G, U = _out(G, "G", shape, X), _out(U, "U", shape, X)
+        ws = _workspace(workspace,
+                        L.hqq_gated_linear_workspace_bytes(M, gate.ptr, up.ptr, 0), gate)
+        st = L.hqq_gated_linear(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), gate.ptr, up.ptr,
+                                code, Y.data_ptr(), _ptr(G), _ptr(U), _ptr(ws), _nbytes(ws),
+                                handle)
+    finally:
+        if on is not None:
+            on.leave(Y, G, U)
+    if st:
+        _check(st, "hqq_gated_linear")
     return Y if G is None else (Y, G, U)
 
 
@@ -766,28 +799,32 @@ def hqq_gated_linear_backward(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor
     """Gradient of hqq_gated_linear from its saved G and U: returns (dX, dG, dU), and with
     bias_grad also the sums of dG and dU over the tokens, (dX, dG, dU, dbias_gate, dbias_up)."""
     code = _act(act)
-    dev = gate.device
-    M = _tokens(dY, "dY", gate.rows, dev)
+    M = _tokens(dY, "dY", gate.rows, gate)
+    _check_weights(dY.dtype, gate, up)
     for name, t in (("G", G), ("U", U)):
         if t.dtype != dY.dtype or t.shape != dY.shape:
             raise ValueError(f"{name} must be like dY")
-        _cuda(t, name, dev)
-    with _Launch(dev, stream, (gate, up), dY.dtype, dY, G, U) as run:
-        dX = run.out(dX, "dX", (*dY.shape[:-1], gate.cols), dY.dtype)
-        dG = run.out(dG, "dG", dY.shape, dY.dtype)
-        dU = run.out(dU, "dU", dY.shape, dY.dtype)
-        db = [run.out(None, "dbias", (gate.rows,), dY.dtype) if bias_grad else None
-              for _ in range(2)]
-        L = lib()
-        need = L.hqq_gated_linear_workspace_bytes(M, gate.ref, up.ref, 1) \
-            if workspace is None else 0
-        wp, wn, _keep = run.workspace(workspace, 0 if need == _NO_SIZE else need)
+        _cuda(t, name, gate.device)
+    L = _lib or lib()
+    handle, on = _begin(gate, stream, dY, G, U)
+    dbg = dbu = None
+    try:
+        dX = _out(dX, "dX", _shape(dY, gate.cols), dY)
+        dG, dU = _out(dG, "dG", dY.shape, dY), _out(dU, "dU", dY.shape, dY)
+        if bias_grad:
+            dbg, dbu = _out(None, "", (gate.rows,), dY), _out(None, "", (gate.rows,), dY)
+        ws = _workspace(workspace,
+                        L.hqq_gated_linear_workspace_bytes(M, gate.ptr, up.ptr, 1), gate)
         st = L.hqq_gated_linear_backward(
-            dY.data_ptr(), G.data_ptr(), U.data_ptr(), M, _TORCH_DT.get(dY.dtype, -1), gate.ref,
-            up.ref, code, dG.data_ptr(), dU.data_ptr(), dX.data_ptr(), _ptr(db[0]), _ptr(db[1]),
-            wp, wn, run.handle)
-    _check(st, "hqq_gated_linear_backward")
-    return (dX, dG, dU, *db) if bias_grad else (dX, dG, dU)
+            dY.data_ptr(), G.data_ptr(), U.data_ptr(), M, _TORCH_DT.get(dY.dtype, -1), gate.ptr,
+            up.ptr, code, dG.data_ptr(), dU.data_ptr(), dX.data_ptr(), _ptr(dbg), _ptr(dbu),
+            _ptr(ws), _nbytes(ws), handle)
+    finally:
+        if on is not None:
+            on.leave(dX, dG, dU, dbg, dbu)
+    if st:
+        _check(st, "hqq_gated_linear_backward")
+    return (dX, dG, dU, dbg, dbu) if bias_grad else (dX, dG, dU)
 
 
 def hqq_wait_timeouts() -> int:

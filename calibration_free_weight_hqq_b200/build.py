@@ -22,7 +22,8 @@ SOURCES = ["hqq_abi.cu", "hqq_quantize.cu", "hqq_quantize_stop.cu", "hqq_dequant
            "hqq_few_1.cu", "hqq_few_2.cu", "hqq_few_3.cu", "hqq_few_4.cu", "hqq_few_8.cu",
            "hqq_dense.cu"]
 HEADERS = ["hqq_device.cuh", "hqq_tensor.cuh", "hqq_act.cuh", "hqq_kernels.h",
-           "hqq_quantize_impl.cuh", "hqq_few_impl.cuh", "hqq_abi_internal.h"]
+           "hqq_quantize_impl.cuh", "hqq_few.h", "hqq_few_impl.cuh",
+           "hqq_abi_internal.h"]
 PUBLIC_HEADER = os.path.join(ROOT, "include", "hqq", "hqq.h")
 
 NVCC_FLAGS = [

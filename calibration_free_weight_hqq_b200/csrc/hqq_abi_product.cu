@@ -19,9 +19,6 @@ using hqqabi::cuda_status;
 
 namespace {
 
-// Tokens up to which the few-token kernel serves a product (see use_few).
-constexpr int64_t kFewMaxTokens = 32;
-
 constexpr int64_t kMaxDim = int64_t(1) << 31;
 
 size_t weight_bytes(const hqq_weight& w) {  // the dequantized weight, 256-byte aligned
@@ -77,24 +74,6 @@ bool same_format(const hqq_params& a, const hqq_params& b) {
          ((!a.quant_scale && !a.quant_zero) || a.meta_group_size == b.meta_group_size);
 }
 
-// Whether a forward product runs on the few-token kernel: groups along the rows, one format,
-// few tokens. A weight of no columns has an empty sum in either kernel; that one writes it.
-bool use_few(int64_t M, const hqq_weight& w, const hqq_weight* up) {
-  if (w.cols == 0) return true;
-  if (M > kFewMaxTokens || w.params.axis != 1) return false;
-  return up == nullptr || same_format(w.params, up->params);
-}
-
-size_t forward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
-  if (M == 0 || use_few(M, w, up)) return 0;
-  return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
-}
-
-size_t backward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
-  if (M == 0) return 0;
-  return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
-}
-
 hqqk::WeightView view(const hqq_weight& w) {
   hqqk::WeightView v;
   v.packed = static_cast<const uint8_t*>(w.Wq_packed);
@@ -104,6 +83,38 @@ hqqk::WeightView view(const hqq_weight& w) {
   v.zero_mm = w.params.quant_zero ? static_cast<const float*>(w.zero_mm) : nullptr;
   v.bias = w.bias;
   return v;
+}
+
+hqqk::FewJob few_job(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  hqqk::FewJob j = {};
+  j.w[0] = view(w);
+  if (up) j.w[1] = view(*up);
+  j.mats = up ? 2 : 1;
+  j.M = M;
+  j.N = w.rows;
+  j.K = w.cols;
+  j.nbits = w.params.nbits;
+  j.group_size = w.params.group_size;
+  j.meta_dtype = w.params.meta_dtype;
+  j.meta_group_size = std::max(w.params.meta_group_size, 1);
+  return j;
+}
+
+// Whether a forward product runs on the few-token kernel: groups along the rows, one format,
+// few tokens.
+bool use_few(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  return w.params.axis == 1 && (up == nullptr || same_format(w.params, up->params)) &&
+         hqqk::few_serves(few_job(M, w, up));
+}
+
+size_t forward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  if (M == 0 || w.cols == 0 || use_few(M, w, up)) return 0;
+  return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
+}
+
+size_t backward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  if (M == 0) return 0;
+  return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
 }
 
 hqqk::DequantJob dequant_job(const hqq_weight& w, int dtype, void* out) {
@@ -147,26 +158,6 @@ hqq_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   return aligned(workspace, 16) ? HQQ_OK : HQQ_ERR_ALIGNMENT;
 }
 
-// The few-token kernel over any number of tokens (its grid holds 65535 tiles of them).
-hqq_status run_few(hqqk::FewJob j, cudaStream_t stream) {
-  constexpr int64_t kChunk = 65535 * 8;
-  const int64_t M = j.M;
-  auto at = [](void* p, int64_t elems) {
-    return p == nullptr ? nullptr : static_cast<void*>(static_cast<char*>(p) + 2 * elems);
-  };
-  const hqqk::FewJob whole = j;
-  for (int64_t m = 0; m < M; m += kChunk) {
-    j.M = std::min<int64_t>(kChunk, M - m);
-    j.X = static_cast<const char*>(whole.X) + 2 * m * j.K;
-    j.Y = at(whole.Y, m * j.N);
-    j.G = at(whole.G, m * j.N);
-    j.U = at(whole.U, m * j.N);
-    const hqq_status st = cuda_status(hqqk::launch_few(j, stream));
-    if (st != HQQ_OK) return st;
-  }
-  return HQQ_OK;
-}
-
 hqq_status forward(const void* X, int64_t M, int dtype, const hqq_weight& w, const hqq_weight* up,
                    int act, void* Y, void* G, void* U, void* workspace, size_t workspace_bytes,
                    cudaStream_t stream) {
@@ -177,25 +168,20 @@ hqq_status forward(const void* X, int64_t M, int dtype, const hqq_weight& w, con
   hqq_status st = check_workspace(workspace, workspace_bytes, forward_need(M, w, up));
   if (st != HQQ_OK) return st;
   if ((st = check_device(w.cols > 0 ? X : Y)) != HQQ_OK) return st;
+  if (w.cols == 0) {
+    const void* const bias[2] = {w.bias, up ? up->bias : nullptr};
+    return cuda_status(hqqk::launch_empty_sums(bias, up ? 2 : 1, M, w.rows, dtype, act, Y, G, U,
+                                               stream));
+  }
   if (use_few(M, w, up)) {
-    hqqk::FewJob j = {};
+    hqqk::FewJob j = few_job(M, w, up);
     j.X = X;
-    j.w[0] = view(w);
-    if (up) j.w[1] = view(*up);
-    j.mats = up ? 2 : 1;
-    j.M = M;
-    j.N = w.rows;
-    j.K = w.cols;
     j.x_dtype = dtype;
-    j.nbits = w.params.nbits;
-    j.group_size = w.params.group_size;
-    j.meta_dtype = w.params.meta_dtype;
-    j.meta_group_size = std::max(w.params.meta_group_size, 1);
     j.act = act;
     j.Y = Y;
     j.G = G;
     j.U = U;
-    return run_few(j, stream);
+    return cuda_status(hqqk::launch_few(j, stream));
   }
   hqqk::DenseJob j = {};
   if ((st = dequantize_into(workspace, w, up, dtype, j.B, stream)) != HQQ_OK) return st;

@@ -488,6 +488,32 @@ cudaError_t launch_gated_grad_typed(const void* dY, const void* G, const void* U
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------- empty sums
+template <bool F16>
+__global__ void __launch_bounds__(256)
+    empty_sums_kernel(const unsigned short* bg, const unsigned short* bu, int mats, int64_t total,
+                      int64_t N, int act, unsigned short* Y, unsigned short* G, unsigned short* U) {
+  constexpr int OUT = F16 ? kF16 : kBF16;
+  auto bits = [](float f) { return static_cast<unsigned short>(pack2_16<OUT>(f, 0.0f)); };
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t n = i % N;
+    const unsigned short hg = bg != nullptr ? bg[n] : 0, hu = bu != nullptr ? bu[n] : 0;
+    if (mats == 1) {
+      Y[i] = hg;
+      continue;
+    }
+    const float g = F16 ? f16_bits_to_f32(hg) : bf16_bits_to_f32(hg);
+    const float u = F16 ? f16_bits_to_f32(hu) : bf16_bits_to_f32(hu);
+    const float h = act == kSilu   ? act_f32<kSilu>(g)
+                    : act == kGelu ? act_f32<kGelu>(g)
+                                   : act_f32<kGeluTanh>(g);
+    Y[i] = bits(__fmul_rn(h, u));
+    if (G != nullptr) G[i] = hg;
+    if (U != nullptr) U[i] = hu;
+  }
+}
+
 // ---------------------------------------------------------------- column sums
 // A block owns 64 columns: 8 threads of 8 columns side by side (128-byte lines), 32 rows at a
 // time; each thread adds its rows in order, then the 32 partial sums are added in order.
@@ -536,6 +562,20 @@ cudaError_t launch_gated_grad(const void* dY, const void* G, const void* U, int6
   if (n == 0) return cudaSuccess;
   return x_dtype == kF16 ? launch_gated_grad_typed<true>(dY, G, U, n, act, dG, dU, st)
                          : launch_gated_grad_typed<false>(dY, G, U, n, act, dG, dU, st);
+}
+
+cudaError_t launch_empty_sums(const void* const (&bias)[2], int mats, int64_t M, int64_t N,
+                              int x_dtype, int act, void* Y, void* G, void* U, cudaStream_t st) {
+  const auto *bg = static_cast<const unsigned short*>(bias[0]),
+             *bu = static_cast<const unsigned short*>(bias[1]);
+  auto *y = static_cast<unsigned short*>(Y), *g = static_cast<unsigned short*>(G),
+       *u = static_cast<unsigned short*>(U);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((M * N + 255) / 256, 148 * 8));
+  if (x_dtype == kF16)
+    empty_sums_kernel<true><<<grid, 256, 0, st>>>(bg, bu, mats, M * N, N, act, y, g, u);
+  else
+    empty_sums_kernel<false><<<grid, 256, 0, st>>>(bg, bu, mats, M * N, N, act, y, g, u);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_column_sum(const void* A, int64_t rows, int64_t cols, int x_dtype, void* out,

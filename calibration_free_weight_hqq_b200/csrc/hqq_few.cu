@@ -1,4 +1,5 @@
 // hqq_few.cu - picks the few-token product's instantiation by code width (hqq_few_impl.cuh).
+#include "hqq_few.h"
 #include "hqq_kernels.h"
 
 namespace hqqk {
@@ -10,6 +11,8 @@ extern template cudaError_t launch_few_bits<2>(const FewJob&, cudaStream_t);
 extern template cudaError_t launch_few_bits<3>(const FewJob&, cudaStream_t);
 extern template cudaError_t launch_few_bits<4>(const FewJob&, cudaStream_t);
 extern template cudaError_t launch_few_bits<8>(const FewJob&, cudaStream_t);
+
+bool few_serves(const FewJob& j) { return few_warps(j) > 0; }
 
 cudaError_t launch_few(const FewJob& j, cudaStream_t st) {
   switch (j.nbits) {

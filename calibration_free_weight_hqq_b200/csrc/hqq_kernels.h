@@ -83,7 +83,7 @@ struct WeightView {
   const void* bias;
 };
 
-// Few-token product over one weight (mats = 1: Y = X W'^T + bias) or the gated pair (mats = 2:
+// Product of up to 8 tokens with one weight (mats = 1: Y = X W'^T + bias) or the gated pair (mats = 2:
 // Y = act(X Wg'^T + bg) * (X Wu'^T + bu)); axis 1, any nbits and group size, both weights of
 // one format. G, U: nullptr or where the gated pair's projections go, rounded.
 struct FewJob {
@@ -96,6 +96,8 @@ struct FewJob {
   int act;
   void *Y, *G, *U;
 };
+// Whether launch_few takes a job of these sizes and format (up to 8 tokens whose X fits).
+bool few_serves(const FewJob& job);
 cudaError_t launch_few(const FewJob& job, cudaStream_t stream);
 
 // Large products on dequantized weights (x_dtype, row-major), on the 2-SM tensor-core kernel.
@@ -117,6 +119,11 @@ struct DenseJob {
 };
 cudaError_t launch_dense(const DenseJob& job, cudaStream_t stream);
 cudaError_t read_dense_timeouts(unsigned int* out);
+
+// Products over weights of no columns: every sum is its bias (or 0).
+cudaError_t launch_empty_sums(const void* const (&bias)[2], int mats, int64_t M, int64_t N,
+                              int x_dtype, int act, void* Y, void* G, void* U,
+                              cudaStream_t stream);
 
 // dG = dY * U * act'(G), dU = dY * act(G), elementwise over n values of x_dtype.
 cudaError_t launch_gated_grad(const void* dY, const void* G, const void* U, int64_t n, int x_dtype,
