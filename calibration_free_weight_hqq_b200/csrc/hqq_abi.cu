@@ -10,6 +10,7 @@
 #include "../../include/hqq/hqq.h"
 #include "hqq_abi_internal.h"
 #include "hqq_kernels.h"
+#include "hqq_mid.h"
 
 #define HQQ_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -575,10 +576,11 @@ HQQ_EXPORT hqq_status hqq_linear(const void* X, int64_t M, int64_t K, hqq_dtype 
 
 HQQ_EXPORT hqq_status hqq_wait_timeouts(unsigned int* count) {
   if (!count) return HQQ_ERR_INVALID_ARG;
-  unsigned int gemm = 0, dense = 0;
+  unsigned int gemm = 0, dense = 0, mid = 0;
   hqq_status st = cuda_status(hqqk::read_gemm_timeouts(&gemm));
   if (st == HQQ_OK) st = cuda_status(hqqk::read_dense_timeouts(&dense));
-  if (st == HQQ_OK) *count = gemm + dense;
+  if (st == HQQ_OK) st = cuda_status(hqqk::read_mid_timeouts(&mid));
+  if (st == HQQ_OK) *count = gemm + dense + mid;
   return st;
 }
 

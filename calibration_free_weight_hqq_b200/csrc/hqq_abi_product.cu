@@ -6,6 +6,7 @@
 #include "../../include/hqq/hqq.h"
 #include "hqq_abi_internal.h"
 #include "hqq_kernels.h"
+#include "hqq_mid.h"
 
 #define HQQ_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -107,14 +108,50 @@ bool use_few(int64_t M, const hqq_weight& w, const hqq_weight* up) {
          hqqk::few_serves(few_job(M, w, up));
 }
 
-size_t forward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
-  if (M == 0 || w.cols == 0 || use_few(M, w, up)) return 0;
+// Tokens up to which the some-token kernel serves a product it can take.
+constexpr int64_t kMidMaxTokens = 1024;
+
+hqqk::MidJob mid_job(int mode, int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  hqqk::MidJob j = {};
+  j.mode = mode;
+  j.w[0] = view(w);
+  if (up) j.w[1] = view(*up);
+  j.weights = up ? 2 : 1;
+  j.M = M;
+  j.rows = w.rows;
+  j.cols = w.cols;
+  j.nbits = w.params.nbits;
+  j.group_size = w.params.group_size;
+  j.meta_dtype = w.params.meta_dtype;
+  j.meta_group_size = std::max(w.params.meta_group_size, 1);
+  return j;
+}
+
+// Whether a product runs straight from the codes on the some-token kernel, and what workspace
+// that takes.
+bool use_mid(int mode, int64_t M, const hqq_weight& w, const hqq_weight* up, size_t* need) {
+  if (M > kMidMaxTokens || w.params.axis != 1) return false;
+  if (up != nullptr && !same_format(w.params, up->params)) return false;
+  hqqk::MidPlan plan;
+  if (!hqqk::mid_plan(mid_job(mode, M, w, up), &plan)) return false;
+  *need = (plan.partial_bytes + 255) / 256 * 256;
+  return true;
+}
+
+size_t dense_need(const hqq_weight& w, const hqq_weight* up) {
   return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
 }
 
+size_t forward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  size_t need = 0;
+  if (M == 0 || w.rows == 0 || w.cols == 0 || use_few(M, w, up)) return 0;
+  return use_mid(up ? hqqk::kMidGated : hqqk::kMidLinear, M, w, up, &need) ? need : dense_need(w, up);
+}
+
 size_t backward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
-  if (M == 0) return 0;
-  return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
+  size_t need = 0;
+  if (M == 0 || w.rows == 0 || w.cols == 0) return 0;
+  return use_mid(hqqk::kMidBackward, M, w, up, &need) ? need : dense_need(w, up);
 }
 
 hqqk::DequantJob dequant_job(const hqq_weight& w, int dtype, void* out) {
@@ -183,6 +220,18 @@ hqq_status forward(const void* X, int64_t M, int dtype, const hqq_weight& w, con
     j.U = U;
     return cuda_status(hqqk::launch_few(j, stream));
   }
+  const int mode = up ? hqqk::kMidGated : hqqk::kMidLinear;
+  if (size_t need = 0; use_mid(mode, M, w, up, &need)) {
+    hqqk::MidJob j = mid_job(mode, M, w, up);
+    j.X[0] = X;
+    j.x_dtype = dtype;
+    j.act = act;
+    j.Y = Y;
+    j.G = G;
+    j.U = U;
+    j.workspace = workspace;
+    return cuda_status(hqqk::launch_mid(j, stream));
+  }
   hqqk::DenseJob j = {};
   if ((st = dequantize_into(workspace, w, up, dtype, j.B, stream)) != HQQ_OK) return st;
   j.kind = up ? hqqk::kDenseGated : hqqk::kDenseForward;
@@ -207,6 +256,15 @@ hqq_status backward(const void* const (&A)[2], int64_t M, int dtype, const hqq_w
   if (M == 0 || w.cols == 0) return HQQ_OK;
   if (w.rows == 0)  // an empty sum
     return cuda_status(cudaMemsetAsync(dX, 0, static_cast<size_t>(M) * w.cols * 2, stream));
+  if (size_t need = 0; use_mid(hqqk::kMidBackward, M, w, up, &need)) {
+    hqqk::MidJob j = mid_job(hqqk::kMidBackward, M, w, up);
+    j.X[0] = A[0];
+    j.X[1] = A[1];
+    j.x_dtype = dtype;
+    j.Y = dX;
+    j.workspace = workspace;
+    return cuda_status(hqqk::launch_mid(j, stream));
+  }
   hqqk::DenseJob j = {};
   const hqq_status st = dequantize_into(workspace, w, up, dtype, j.B, stream);
   if (st != HQQ_OK) return st;

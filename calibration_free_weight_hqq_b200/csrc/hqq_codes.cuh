@@ -1,0 +1,392 @@
+// hqq_codes.cuh - packed codes of any width to W' in registers: loading, widening, scale and zero,
+// with exactly the dequantizer's roundings. Shared by the products that multiply straight from the
+// codes. Everything has internal linkage.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "hqq_device.cuh"
+#include "hqq_kernels.h"
+#include "hqq_tiles.h"
+
+namespace hqqk {
+namespace {
+
+// Up to two weights of one format.
+struct WeightArgs {
+  const uint8_t* packed[2];
+  const void* scale[2];
+  const void* zero[2];
+  const float2* scale_mm[2];
+  const float2* zero_mm[2];
+  const unsigned short* bias[2];
+  int lg_group;   // log2 of the group size
+  int meta_dt;    // Dt of scale / zero where they are not 8-bit codes
+  int meta_run;   // second-level run length, and its log2 (-1: no power of two)
+  int lg_run;
+};
+
+// The codes of 32 consecutive elements: 32-bit words, least significant code first (8, 4, 2, 1 bits:
+// NBITS words); 3 bits: one 24-bit field of 8 codes per word.
+template <int NBITS>
+struct Codes32 {
+  static constexpr int kWords = NBITS == 3 ? 4 : NBITS;
+  uint32_t w[kWords];
+};
+
+// A code is widened by making its bits the mantissa of a half-precision power of two, where they
+// stand: at bits 0 .. of a half under 1024 they read 1024 + q, at bits NBITS .. under
+// 2^(10 - NBITS) they read that plus q, exactly; one shift serves two masks, and each mask takes two
+// codes, 16 bits apart. Pair p of unit u (8 MMA k slots) holds the elements
+//   8 and 3 bits  8u + 2p, 8u + 2p + 1            2 bits  16(u/2) + 4(u%2) + p, 8 further
+//   4 bits        8u + p, 8u + p + 4              1 bit   4u + p, 16 further
+// of its chunk of 32, and X is laid out in the same order (slot_element).
+template <int NBITS>
+__host__ __device__ constexpr int slot_element(int u, int j) {  // slot j = 0 .. 7 of unit u
+  const int p = j / 2, h = j % 2;
+  return NBITS == 4   ? 8 * u + p + 4 * h
+         : NBITS == 2 ? 16 * (u / 2) + 4 * (u % 2) + p + 8 * h
+         : NBITS == 1 ? 4 * u + p + 16 * h
+                      : 8 * u + j;
+}
+// (v & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+  return d;
+}
+// The base under a code of pair p.
+template <int NBITS>
+__host__ __device__ constexpr float slot_base(int p) {
+  return NBITS == 8 || NBITS == 3 || p % 2 == 0 ? 1024.0f : static_cast<float>(1 << (10 - NBITS % 8));
+}
+template <int NBITS>
+__device__ __forceinline__ uint32_t widened_pair(const Codes32<NBITS>& c, int u, int p) {
+  constexpr uint32_t k1024 = 0x64006400u;
+  if constexpr (NBITS == 8) {
+    return __byte_perm(c.w[2 * u + p / 2], k1024, p % 2 ? 0x5352 : 0x5150);
+  } else if constexpr (NBITS == 3) {
+    const uint32_t f = c.w[u];
+    const int hi = 6 * p + 3 - 16;  // the second code's way to bit 16
+    return and_or(hi < 0 ? f << -hi : f >> hi, 0x00070000u, and_or(f >> (6 * p), 7u, k1024));
+  } else {
+    constexpr uint32_t kMask = ((1u << NBITS) - 1u) * 0x00010001u;
+    constexpr uint32_t kOdd = k1024 - static_cast<uint32_t>(NBITS) * 0x04000400u;  // 2^(10 - NBITS)
+    // code j of the pair's word, counted in pairs
+    const int j = NBITS == 4 ? p : NBITS == 2 ? 4 * (u % 2) + p : 4 * u + p;
+    const uint32_t v = c.w[NBITS == 4 ? u : NBITS == 2 ? u / 2 : 0] >> (NBITS * (j - p % 2));
+    return p % 2 ? and_or(v, kMask << NBITS, kOdd) : and_or(v, kMask, k1024);
+  }
+}
+
+// c + a half-precision value in fp32, rounded once.
+__device__ __forceinline__ float2 add_f32_f16x2(uint32_t h, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "add.rn.f32.f16 %0, lo, %3;\n\tadd.rn.f32.f16 %1, hi, %4;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(h), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// A group's scale and zero as the conversion takes them. Where base + zero is exact,
+// (base + q) - (base + zero) is the one rounding of q - zero (`even`, `odd` alone, by the pair's
+// base); otherwise the base is subtracted first, exactly, and then zero. If 1024 + zero is exact, so
+// is the sum with the smaller base. The test is cheap and, for zeros of 8 or 11 significant bits,
+// fails only next to 0.
+struct GroupMeta {
+  float scale, even, odd, neg_zero;
+};
+template <int NBITS>
+__device__ __forceinline__ GroupMeta group_meta(float scale, float zero, bool* one) {
+  const float sum = __fadd_rn(zero, 1024.0f);
+  *one = *one && __fsub_rn(sum, 1024.0f) == zero;
+  return GroupMeta{scale, -sum, -__fadd_rn(zero, slot_base<NBITS>(1)), -zero};
+}
+
+// Pair p of unit u as W' in fp32, with the dequantizer's first two roundings: q - zero, * scale. m: the
+// chunk's GROUPS groups.
+template <int NBITS, int GROUPS, bool ONE>
+__device__ __forceinline__ float2 dequant_pair(const Codes32<NBITS>& c, int u, int p,
+                                               const GroupMeta* m) {
+  const GroupMeta& a = m[slot_element<NBITS>(u, 2 * p) * GROUPS / 32];
+  const GroupMeta& b = m[slot_element<NBITS>(u, 2 * p + 1) * GROUPS / 32];
+  const uint32_t h = widened_pair<NBITS>(c, u, p);
+  float2 v;
+  if constexpr (ONE)
+    v = add_f32_f16x2(h, p % 2 ? make_float2(a.odd, b.odd) : make_float2(a.even, b.even));
+  else
+    v = fadd2_rn(add_f32_f16x2(h, make_float2(-slot_base<NBITS>(p), -slot_base<NBITS>(p))),
+                 make_float2(a.neg_zero, b.neg_zero));
+  return fmul2_rn(v, make_float2(a.scale, b.scale));
+}
+
+// Unit u of a chunk as W' pairs in slot order, rounded to dt.
+template <int NBITS, int OUT, int GROUPS, bool ONE>
+__device__ __forceinline__ uint4 dequant_unit(const Codes32<NBITS>& c, int u, const GroupMeta* m) {
+  uint32_t o[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float2 v = dequant_pair<NBITS, GROUPS, ONE>(c, u, p, m);
+    o[p] = pack2_16<OUT>(v.x, v.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// All 32 codes of a chunk as W', in their own order: eight to a uint4.
+template <int NBITS, int OUT, int GROUPS, bool ONE>
+__device__ __forceinline__ void dequant_chunk(const Codes32<NBITS>& c, const GroupMeta* m,
+                                              uint4 (&o)[4]) {
+  float2 v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = dequant_pair<NBITS, GROUPS, ONE>(c, i / 4, i % 4, m);
+  auto four = [](float2 a, float2 b, float2 c, float2 d) {
+    return make_uint4(pack2_16<OUT>(a.x, a.y), pack2_16<OUT>(b.x, b.y), pack2_16<OUT>(c.x, c.y),
+                      pack2_16<OUT>(d.x, d.y));
+  };
+  auto lows = [&](int i) { return make_float2(v[i].x, v[i + 1].x); };
+  auto highs = [&](int i) { return make_float2(v[i].y, v[i + 1].y); };
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if constexpr (NBITS == 4)
+      o[u] = four(lows(4 * u), lows(4 * u + 2), highs(4 * u), highs(4 * u + 2));
+    else if constexpr (NBITS == 2)
+      o[u] = u % 2 == 0 ? four(lows(4 * u), lows(4 * u + 2), lows(4 * u + 4), lows(4 * u + 6))
+                        : four(highs(4 * u - 4), highs(4 * u - 2), highs(4 * u), highs(4 * u + 2));
+    else if constexpr (NBITS == 1)
+      o[u] = u < 2 ? four(lows(8 * u), lows(8 * u + 2), lows(8 * u + 4), lows(8 * u + 6))
+                   : four(highs(8 * u - 16), highs(8 * u - 14), highs(8 * u - 12), highs(8 * u - 10));
+    else
+      o[u] = four(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+  }
+}
+
+// Copies through L1: a lane's 32 contiguous bytes are one sector in two pieces, and bypassing L1 would
+// fetch it twice (28672 x 4096, one token: 32 -> 28 us).
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Copies a lane's 32 codes into its own shared-memory slot: from byte `off` of `base` on or, at
+// 3 bits, from element `off` on counted from the first code of the word at `base`. Row lengths are
+// multiples of 32 codes, so every copy is aligned to its width. A slot's pieces lie 32 lanes apart, so
+// that a warp's pieces are contiguous. `slot` points at the lane's first piece.
+template <int NBITS>
+__device__ __forceinline__ void copy_chunk(uint32_t slot, const uint8_t* base, uint32_t off) {
+  if constexpr (NBITS == 3) {
+    const uint32_t word = off / 10u, first = off - word * 10u;
+    const uint8_t* p = base + word * 4u;
+#pragma unroll
+    for (int i = 0; i < 5; ++i)  // 31 codes further: the fifth word only from slot 9
+      if (i < 4 || first == 9u) cp_async<4>(slot + i * 128, p + 4 * i);
+  } else {
+    constexpr int kPiece = NBITS >= 4 ? 16 : 4 * NBITS;
+#pragma unroll
+    for (int i = 0; i < 4 * NBITS / kPiece; ++i)
+      cp_async<kPiece>(slot + i * 32 * kPiece, base + off + i * kPiece);
+  }
+}
+
+// The chunk in a lane's slot (3 bits: `off` as it was copied).
+template <int NBITS>
+__device__ __forceinline__ Codes32<NBITS> read_chunk(const uint8_t* slot, uint32_t off) {
+  Codes32<NBITS> c;
+  if constexpr (NBITS == 3) {
+    uint32_t v[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = *reinterpret_cast<const uint32_t*>(slot + 128 * i);
+    const int first_slot = static_cast<int>(off % 10u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int at = first_slot + 8 * u;      // 8u .. 8u + 9
+      const int first = 8 * u / 10;           // the word of code 8u, or the next one
+      const bool next = at >= 10 * (first + 1);
+      const int s = at - 10 * (first + (next ? 1 : 0));
+      const uint32_t lo = next ? v[first + 1] : v[first];
+      const uint32_t hi = next ? v[first + 2 < 5 ? first + 2 : 4] : v[first + 1];
+      c.w[u] = (lo & 0x3FFFFFFFu) >> (3 * s) | hi << (30 - 3 * s);
+    }
+  } else if constexpr (NBITS >= 4) {
+#pragma unroll
+    for (int i = 0; i < NBITS / 4; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(slot + 512 * i);
+      c.w[4 * i] = v.x;
+      c.w[4 * i + 1] = v.y;
+      c.w[4 * i + 2] = v.z;
+      c.w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (NBITS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(slot);
+    c.w[0] = v.x;
+    c.w[1] = v.y;
+  } else {
+    c.w[0] = *reinterpret_cast<const uint32_t*>(slot);
+  }
+  return c;
+}
+
+// As above for rows of any multiple of 8 codes, in units of 8 codes (NBITS bytes, aligned to their
+// size): the first `units` of the chunk exist, the others read as code 0.
+template <int NBITS>
+__device__ __forceinline__ Codes32<NBITS> load_codes_units(const uint8_t* slab, uint32_t e,
+                                                           int units) {
+  Codes32<NBITS> c;
+#pragma unroll
+  for (int i = 0; i < Codes32<NBITS>::kWords; ++i) c.w[i] = 0u;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u >= units) break;
+    if constexpr (NBITS == 3) {
+      const uint32_t word = (e + 8u * u) / 10u;
+      const int s = static_cast<int>(e + 8u * u - word * 10u);
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(slab) + word;
+      const uint32_t lo = __ldg(p) & 0x3FFFFFFFu;
+      const uint32_t hi = s > 2 ? __ldg(p + 1) : 0u;  // 8 codes from slot 2 end in this word
+      c.w[u] = lo >> (3 * s) | hi << (30 - 3 * s);
+    } else {
+      const uint8_t* p = slab + static_cast<uint64_t>((e / 8u + u) * NBITS);
+      if constexpr (NBITS == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        c.w[2 * u] = v.x;
+        c.w[2 * u + 1] = v.y;
+      } else if constexpr (NBITS == 4) {
+        c.w[u] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else if constexpr (NBITS == 2) {
+        c.w[u / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p)))
+                      << (16 * (u % 2));
+      } else {
+        c.w[0] |= static_cast<uint32_t>(__ldg(p)) << (8 * u);
+      }
+    }
+  }
+  return c;
+}
+
+// Consecutive rows of one weight: their codes and meta, addressed by 32-bit offsets from here.
+struct Slab {
+  const uint8_t* codes;   // see copy_chunk
+  const uint8_t *scale, *zero;
+  const float2 *scale_mm, *zero_mm;  // from the run of the slab's first group on, or nullptr
+  uint32_t code0;         // 3 bits: slot of the slab's first code in its word
+  uint32_t group0;        // the first group's place in its run
+};
+
+// The slab of the rows from `row` on of matrix i.
+template <int NBITS, bool ANY>
+__device__ __forceinline__ Slab slab_of_row(const WeightArgs& a, int i, int64_t row, uint32_t K,
+                                            uint32_t groups_per_row) {
+  const int64_t e0 = row * K, g0 = row * groups_per_row;
+  const uint32_t msz = ANY && a.meta_dt == kF32 ? 4 : 2;
+  Slab b;
+  b.code0 = NBITS == 3 ? static_cast<uint32_t>(e0 % 10) : 0u;
+  b.codes = a.packed[i] + (NBITS == 3 ? e0 / 10 * 4 : e0 / 8 * NBITS);
+  b.scale_mm = b.zero_mm = nullptr;
+  b.group0 = 0;
+  if constexpr (ANY) {
+    const int64_t run0 = g0 / a.meta_run;
+    b.group0 = static_cast<uint32_t>(g0 - run0 * a.meta_run);
+    if (a.scale_mm[i] != nullptr) b.scale_mm = a.scale_mm[i] + run0;
+    if (a.zero_mm[i] != nullptr) b.zero_mm = a.zero_mm[i] + run0;
+  }
+  b.scale = static_cast<const uint8_t*>(a.scale[i]) + g0 * (b.scale_mm != nullptr ? 1 : msz);
+  b.zero = static_cast<const uint8_t*>(a.zero[i]) + g0 * (b.zero_mm != nullptr ? 1 : msz);
+  return b;
+}
+
+// Scale and zero of a group as loaded. ANY false: 16-bit values of the activation type. ANY true:
+// values of any meta type, or 8-bit codes with their run's (step2, zero2).
+template <bool ANY>
+struct RawMeta {
+  uint32_t s, z;
+};
+template <>
+struct RawMeta<true> {
+  uint32_t s, z;
+  float2 sp, zp;
+};
+
+__device__ __forceinline__ uint32_t load_meta_bits(const uint8_t* p, int dt, bool code, uint32_t i) {
+  if (code) return __ldg(p + i);
+  if (dt == kF32) return __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  return __ldg(reinterpret_cast<const unsigned short*>(p) + i);
+}
+__device__ __forceinline__ float meta_value(uint32_t b, int dt) {
+  return dt == kF32 ? __uint_as_float(b) : dt == kBF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
+}
+
+// Group `step + at` of a slab (`step` uniform over the warp).
+template <bool ANY>
+__device__ __forceinline__ RawMeta<ANY> load_raw_meta(const Slab& b, const WeightArgs& a, uint32_t step,
+                                                      uint32_t at) {
+  RawMeta<ANY> m;
+  if constexpr (ANY) {
+    const uint32_t i = step + at, in = b.group0 + i;
+    const uint32_t run = a.lg_run >= 0 ? in >> a.lg_run : in / static_cast<uint32_t>(a.meta_run);
+    m.sp = b.scale_mm != nullptr ? __ldg(b.scale_mm + run) : make_float2(0.0f, 0.0f);
+    m.zp = b.zero_mm != nullptr ? __ldg(b.zero_mm + run) : make_float2(0.0f, 0.0f);
+    m.s = load_meta_bits(b.scale, a.meta_dt, b.scale_mm != nullptr, i);
+    m.z = load_meta_bits(b.zero, a.meta_dt, b.zero_mm != nullptr, i);
+  } else {
+    m.s = __ldg(reinterpret_cast<const unsigned short*>(b.scale + 2u * step + 2u * at));
+    m.z = __ldg(reinterpret_cast<const unsigned short*>(b.zero + 2u * step + 2u * at));
+  }
+  return m;
+}
+
+// (scale, zero) in fp32; 8-bit codes are rebuilt as (code - zero2) * step2.
+template <bool ANY, bool F16>
+__device__ __forceinline__ float2 meta_f32_pair(const RawMeta<ANY>& m, const Slab& b, int dt) {
+  if constexpr (ANY) {
+    const float s = b.scale_mm != nullptr
+                        ? __fmul_rn(__fsub_rn(static_cast<float>(m.s), m.sp.y), m.sp.x)
+                        : meta_value(m.s, dt);
+    const float z = b.zero_mm != nullptr
+                        ? __fmul_rn(__fsub_rn(static_cast<float>(m.z), m.zp.y), m.zp.x)
+                        : meta_value(m.z, dt);
+    return make_float2(s, z);
+  } else {
+    return F16 ? make_float2(f16_bits_to_f32(m.s), f16_bits_to_f32(m.z))
+               : make_float2(bf16_bits_to_f32(m.s), bf16_bits_to_f32(m.z));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// Whether some scale or zero is not simply a value of the activation type (RawMeta's ANY).
+inline bool any_meta(const WeightView* w, int mats, int meta_dtype, int x_dtype) {
+  bool any = meta_dtype != x_dtype;
+  for (int i = 0; i < mats; ++i) any = any || w[i].scale_mm != nullptr || w[i].zero_mm != nullptr;
+  return any;
+}
+
+inline WeightArgs weight_args(const WeightView* w, int mats, int group_size, int meta_dtype,
+                              int meta_group_size) {
+  WeightArgs a = {};
+  for (int i = 0; i < mats; ++i) {
+    a.packed[i] = w[i].packed;
+    a.scale[i] = w[i].scale;
+    a.zero[i] = w[i].zero;
+    a.scale_mm[i] = reinterpret_cast<const float2*>(w[i].scale_mm);
+    a.zero_mm[i] = reinterpret_cast<const float2*>(w[i].zero_mm);
+    a.bias[i] = static_cast<const unsigned short*>(w[i].bias);
+  }
+  a.lg_group = __builtin_ctz(static_cast<unsigned>(group_size));
+  a.meta_dt = meta_dtype;
+  a.meta_run = meta_group_size;
+  a.lg_run = (meta_group_size & (meta_group_size - 1)) == 0 ? __builtin_ctz(meta_group_size) : -1;
+  return a;
+}
+
+}  // namespace
+}  // namespace hqqk

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "hqq_kernels.h"
+#include "hqq_tiles.h"
 
 namespace hqqk {
 
@@ -18,12 +19,10 @@ constexpr int kFewRedStride = kFewRows + 4;  // floats per token of a partial ti
                                              // of a fragment fall on 32 different banks
 constexpr int kFewRed = 8 * kFewRedStride * 4;  // bytes of one warp's partial tile
 
-// Bytes that a lane's chunk of 32 codes takes in shared memory (3 bits: the five words it may span).
-__host__ __device__ constexpr int few_chunk(int nbits) { return nbits == 3 ? 20 : 4 * nbits; }
 // k-blocks whose codes are in flight per warp: about 6 KB of them, 96 KB an SM at 16 warps (the
 // memory's latency at full bandwidth asks for about 40), but 1 at least and 4 at most.
 __host__ __device__ constexpr int few_depth(int nbits, int mats) {
-  const int n = 6144 / (128 * mats * few_chunk(nbits));
+  const int n = 6144 / (128 * mats * chunk_bytes(nbits));
   return n < 1 ? 1 : n > 4 ? 4 : n;
 }
 // Bytes of a token's row of X in shared memory (padded by 64).
@@ -34,7 +33,7 @@ __host__ __device__ constexpr uint32_t few_x_row(uint32_t K) {
 __host__ __device__ constexpr size_t few_smem(int nbits, int mats, int warps, int64_t M, int64_t K) {
   return static_cast<size_t>(M) * few_x_row(static_cast<uint32_t>(K)) +
          static_cast<size_t>(warps * mats) *
-             (kFewRed + few_depth(nbits, mats) * 4 * 32 * few_chunk(nbits));
+             (kFewRed + few_depth(nbits, mats) * 4 * 32 * chunk_bytes(nbits));
 }
 
 // Warps of a CTA: 8 with two CTAs an SM where their X fits in half the shared memory (a CTA's

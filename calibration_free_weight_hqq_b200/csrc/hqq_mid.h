@@ -1,0 +1,62 @@
+// hqq_mid.h - tile sizes, shared memory and the division of work of the products of some tokens
+// (hqq_mid_impl.cuh).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "hqq_kernels.h"
+#include "hqq_tiles.h"
+
+namespace hqqk {
+
+constexpr int kMidRows = 128;    // output features per tile: the M of the MMA
+constexpr int kMidBK = 64;       // contraction per k-block: one 128-byte swizzled line
+constexpr int kMidTokens = 256;  // tokens per tile at most: the N of the MMA
+constexpr int kMidWStages = 4;   // W' operand tiles in shared memory
+constexpr int kMidDqWarps = 16;  // two groups of 8 warps, a W' tile each
+constexpr int kMidEpiWarps = 4;
+constexpr int kMidThreads = 32 * (2 + kMidDqWarps + kMidEpiWarps);
+constexpr uint32_t kMidWBytes = kMidRows * kMidBK * 2;
+constexpr int64_t kMidMaxCols = int64_t(1) << 24;  // 32-bit offsets inside a tile's 128 rows
+
+// W' tiles of a warp whose codes are in flight: 48 KB of them a CTA, 8 at most.
+__host__ __device__ constexpr int mid_depth(int nbits) {
+  const int n = 49152 / (32 * kMidDqWarps * chunk_bytes(nbits));
+  return n < 1 ? 1 : n > 8 ? 8 : n;
+}
+
+enum MidMode : int { kMidLinear = 0, kMidGated = 1, kMidBackward = 2 };
+
+// What the host and the device need to agree on. A unit is one k-block of one tile (of both
+// weights in the gated form); the units of all tiles, in order, are dealt out evenly to the
+// CTAs, and a tile that several CTAs share is summed from their partial tiles.
+struct MidPlan {
+  int tok;             // tokens per tile, a multiple of 16
+  int tok_tiles, row_tiles;
+  int kb1, kb;         // k-blocks of one source, of a tile
+  int ctas;
+  int x_stages;
+  uint32_t off_x, off_ring, off_bar, smem;
+  size_t partial_bytes;
+};
+
+struct MidJob {
+  int mode;
+  const void* X[2];  // tokens x contraction; the second of two sources in kMidBackward
+  WeightView w[2];
+  int weights;       // 1 or 2
+  int64_t M, rows, cols;  // tokens; the weights' shape
+  int x_dtype;
+  int nbits, group_size, meta_dtype, meta_group_size;
+  int act;
+  void *Y, *G, *U;   // outputs (kMidBackward: Y is dX)
+  void* workspace;   // MidPlan::partial_bytes
+};
+
+// Whether the kernel takes a job of these sizes, and its plan.
+bool mid_plan(const MidJob& job, MidPlan* plan);
+cudaError_t launch_mid(const MidJob& job, cudaStream_t stream);
+cudaError_t read_mid_timeouts(unsigned int* out);
+
+}  // namespace hqqk
