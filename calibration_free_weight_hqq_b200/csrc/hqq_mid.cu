@@ -19,20 +19,18 @@ bool mid_plan(const MidJob& j, MidPlan* plan) {
   const int64_t tok_tiles = (j.M + kMidTokens - 1) / kMidTokens;
   p.tok = static_cast<int>(((j.M + tok_tiles - 1) / tok_tiles + 15) / 16 * 16);
   const int64_t row_tiles = (out + kMidRows - 1) / kMidRows;
-  p.kb1 = static_cast<int>((inner + kMidBK - 1) / kMidBK);
+  p.kb1 = static_cast<int>((inner + mid_bk(j.mode) - 1) / mid_bk(j.mode));
   p.kb = back ? p.kb1 * j.weights : p.kb1;
   const int64_t units = row_tiles * tok_tiles * p.kb;
   if (units > 0x3FFFFFFF) return false;
   p.tok_tiles = static_cast<int>(tok_tiles);
   p.row_tiles = static_cast<int>(row_tiles);
-  // every SM, but at least four k-blocks each: fewer cost more in partial tiles than they save
-  p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms, units / 4)));
-  const uint32_t ring = 32u * kMidDqWarps * chunk_bytes(j.nbits) * mid_depth(j.nbits);
-  const uint32_t x_bytes = static_cast<uint32_t>(p.tok) * (2 * kMidBK);
-  const uint32_t room = 232448u - 2048u - kMidWStages * kMidWBytes - ring;
-  p.x_stages = static_cast<int>(std::min<uint32_t>(4, room / x_bytes));
-  p.off_x = kMidWStages * kMidWBytes;
-  p.off_ring = p.off_x + p.x_stages * x_bytes;
+  // every SM, but at least two k-blocks each: fewer cost more in partial tiles than they save
+  p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms, units / 2)));
+  const uint32_t ring = 64u * kMidDqWarps * chunk_bytes(j.nbits) * mid_depth(j.nbits);
+  const uint32_t stage = 2 * kMidTileBytes + static_cast<uint32_t>(p.tok) * 2 * mid_bk(j.mode);
+  p.stages = static_cast<int>(std::min<uint32_t>(4, (232448u - 2048u - ring) / stage));
+  p.off_ring = p.stages * stage;
   p.off_bar = p.off_ring + ring;
   p.smem = p.off_bar + 1024 + 1024;  // barriers, TMEM address and flag; slack to align the base
   p.partial_bytes = static_cast<size_t>(p.ctas) * 2 * (j.mode == kMidGated ? 2 : 1) * p.tok *

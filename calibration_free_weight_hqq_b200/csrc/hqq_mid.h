@@ -11,22 +11,26 @@
 namespace hqqk {
 
 constexpr int kMidRows = 128;    // output features per tile: the M of the MMA
-constexpr int kMidBK = 64;       // contraction per k-block: one 128-byte swizzled line
+constexpr int kMidLine = 64;     // contraction per 128-byte swizzled line
 constexpr int kMidTokens = 256;  // tokens per tile at most: the N of the MMA
-constexpr int kMidWStages = 4;   // W' operand tiles in shared memory
-constexpr int kMidDqWarps = 16;  // two groups of 8 warps, a W' tile each
+constexpr int kMidDqWarps = 16;  // two groups of 8 warps, alternate stages
 constexpr int kMidEpiWarps = 4;
 constexpr int kMidThreads = 32 * (2 + kMidDqWarps + kMidEpiWarps);
-constexpr uint32_t kMidWBytes = kMidRows * kMidBK * 2;
+constexpr uint32_t kMidTileBytes = kMidRows * kMidLine * 2;  // a 128 x 64 tile of W'
 constexpr int64_t kMidMaxCols = int64_t(1) << 24;  // 32-bit offsets inside a tile's 128 rows
 
-// W' tiles of a warp whose codes are in flight: 48 KB of them a CTA, 8 at most.
+// Stages of a warp whose codes are in flight: 32 KB of them a CTA, 8 at most.
 __host__ __device__ constexpr int mid_depth(int nbits) {
-  const int n = 49152 / (32 * kMidDqWarps * chunk_bytes(nbits));
+  const int n = 32768 / (64 * kMidDqWarps * chunk_bytes(nbits));
   return n < 1 ? 1 : n > 8 ? 8 : n;
 }
 
 enum MidMode : int { kMidLinear = 0, kMidGated = 1, kMidBackward = 2 };
+
+// Contraction per k-block, a stage: two W' tiles each, of consecutive lines or, in the gated form, of
+// gate and up. (Stages of one tile left the warp that issues the MMAs as the pace: its wait and
+// commit cost some 700 cycles a stage at any token count.)
+__host__ __device__ constexpr int mid_bk(int mode) { return mode == kMidGated ? 64 : 128; }
 
 // What the host and the device need to agree on. A unit is one k-block of one tile (of both
 // weights in the gated form); the units of all tiles, in order, are dealt out evenly to the
@@ -36,8 +40,8 @@ struct MidPlan {
   int tok_tiles, row_tiles;
   int kb1, kb;         // k-blocks of one source, of a tile
   int ctas;
-  int x_stages;
-  uint32_t off_x, off_ring, off_bar, smem;
+  int stages;
+  uint32_t off_ring, off_bar, smem;
   size_t partial_bytes;
 };
 

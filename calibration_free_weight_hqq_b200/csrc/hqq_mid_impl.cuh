@@ -8,9 +8,9 @@
 // dequantized weight to memory and reading it back: W' goes from the codes into shared memory and
 // no further. The roles of the operands swap against the usual product: 128 output features are
 // the M of tcgen05.mma and up to 256 tokens its N, so that any number of tokens uses whole MMAs.
-//   * Two groups of 8 warps convert codes into the 128-byte-swizzled operand layout, one 128 x 64
-//     W' tile (16 KB) after the other: alternate k-blocks, or in the gated form gate and up. A
-//     thread converts 32 consecutive codes. Backward the same bytes are an MN-major operand: the
+//   * Two groups of 8 warps convert codes into the 128-byte-swizzled operand layout, alternate
+//     stages of two 128 x 64 W' tiles (consecutive in k, or in the gated form of gate and up). A
+//     thread converts 64 codes a stage. Backward the same bytes are an MN-major operand: the
 //     contraction runs along the weight's rows, the features along its columns; nothing is
 //     transposed.
 //   * One warp loads X (TMA, same swizzle), one thread issues the MMAs into TMEM, four warps empty
@@ -49,9 +49,7 @@ struct MidArgs {
   MidPlan p;
 };
 
-constexpr int kMidFullW = 0, kMidEmptyW = kMidFullW + kMidWStages, kMidFullX = kMidEmptyW + kMidWStages,
-              kMidEmptyX = kMidFullX + 4, kMidAccFull = kMidEmptyX + 4, kMidAccEmpty = kMidAccFull + 2,
-              kMidBars = kMidAccEmpty + 2;
+constexpr int kMidFull = 0, kMidEmpty = 4, kMidAccFull = 8, kMidAccEmpty = 10, kMidBars = 12;
 
 // K-major, or MN-major (see the same in hqq_dense.cu: 64-column blocks 8 KB apart, 8-line atoms
 // 1 KB apart along the contraction).
@@ -100,8 +98,8 @@ __device__ __forceinline__ void mid_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// GROUP: 32 (groups of 32 codes or more, cols a multiple of 32), 16 (groups of 16, likewise) or 8 (any
-// group size and cols; codes and meta read where they are used). ANY: see RawMeta.
+// GROUP: 64 (groups of 64 codes or more), 32, 16 (cols a multiple of 32 with both) or 8 (any group size
+// and cols; codes and meta read where they are used). ANY: see RawMeta.
 template <int NBITS, bool F16, int MODE, int GROUP, bool ANY>
 __global__ void __launch_bounds__(kMidThreads, 1)
     mid_tokens_kernel(const __grid_constant__ CUtensorMap map_x0,
@@ -109,9 +107,13 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   constexpr int OUT = F16 ? kF16 : kBF16;
   constexpr int MATS = MODE == kMidGated ? 2 : 1;
   constexpr bool kWhole = GROUP != 8;
-  constexpr int kGroups = 32 / GROUP;
+  // A thread converts two chunks of 32 codes a stage: 64 in a row, or in the gated form 32 of either
+  // weight. Their groups:
+  constexpr int kGroups = GROUP >= 32 ? 1 : 32 / GROUP;
+  constexpr bool kShared = MODE != kMidGated && GROUP >= 64;  // both chunks lie in one group
+  constexpr int kBK = mid_bk(MODE);
   constexpr int kDepth = mid_depth(NBITS);
-  constexpr int kSlot = 32 * chunk_bytes(NBITS);  // a warp's chunks of a W' tile
+  constexpr int kSlot = 32 * chunk_bytes(NBITS);  // a warp's chunks of one kind
   constexpr int kPiece = NBITS == 3 ? 4 : NBITS >= 4 ? 16 : 4 * NBITS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -122,20 +124,17 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   const uint32_t units = static_cast<uint32_t>(a.p.row_tiles * a.p.tok_tiles) * KB;
   const uint32_t first = mid_first_unit(blockIdx.x, gridDim.x, units);
   const uint32_t count = mid_first_unit(blockIdx.x + 1, gridDim.x, units) - first;
-  const uint32_t x_stages = static_cast<uint32_t>(a.p.x_stages), x_bytes = T * (2 * kMidBK);
+  const uint32_t stages = static_cast<uint32_t>(a.p.stages);
+  const uint32_t line_x = T * (2 * kMidLine), stage_bytes = 2 * kMidTileBytes + T * (2 * kBK);
   const uint32_t bufs = 2 * MATS * T <= 512 ? 2 : 1;
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(smem + a.p.off_bar + 8 * kMidBars + 4);
   auto bar = [&](uint32_t i) { return sbase + a.p.off_bar + 8u * i; };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMidWStages; ++s) {
-      mbar_init(bar(kMidFullW + s), kMidDqWarps / 2);
-      mbar_init(bar(kMidEmptyW + s), 1);
-    }
     for (int s = 0; s < 4; ++s) {
-      mbar_init(bar(kMidFullX + s), 1);
-      mbar_init(bar(kMidEmptyX + s), 1);
+      mbar_init(bar(kMidFull + s), kMidDqWarps / 2 + 1);  // the converting warps and the copy of X
+      mbar_init(bar(kMidEmpty + s), 1);                   // the MMAs' commit
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(kMidAccFull + s), 1);
@@ -154,82 +153,97 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + a.p.off_bar + 8 * kMidBars);
+  const uint32_t tmem = __shfl_sync(
+      0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(smem + a.p.off_bar + 8 * kMidBars), 0);
+
+  // mid_finish_kernel may take its place now; it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------------------ X producer
-    uint32_t tile = first / KB, kb = first - tile * KB, pos = 0;
+    uint32_t tile = first / KB, kb = first - tile * KB, pos = 0, s = 0, phase = 1;
+    int m0 = static_cast<int>((tile % a.p.tok_tiles) * T);
     for (; pos < count; ++pos) {
-      const uint32_t s = pos % x_stages;
-      if (!mbar_wait(bar(kMidEmptyX + s), ((pos / x_stages) & 1) ^ 1, abort_flag)) break;
+      if (!mbar_wait(bar(kMidEmpty + s), phase, abort_flag)) break;
       if (lane == 0) {
         const bool second = MODE == kMidBackward && kb >= static_cast<uint32_t>(a.p.kb1);
-        const int k = static_cast<int>(second ? kb - a.p.kb1 : kb) * kMidBK;
-        const int m0 = static_cast<int>((tile % a.p.tok_tiles) * T);
-        mbar_arrive_tx(bar(kMidFullX + s), x_bytes);
-        tma_load_2d(sbase + a.p.off_x + s * x_bytes, second ? &map_x1 : &map_x0, k, m0,
-                    bar(kMidFullX + s));
+        const CUtensorMap* map = second ? &map_x1 : &map_x0;
+        const int k = static_cast<int>(second ? kb - a.p.kb1 : kb) * kBK;
+        const uint32_t dst = sbase + s * stage_bytes + 2 * kMidTileBytes;
+        mbar_arrive_tx(bar(kMidFull + s), T * (2 * kBK));
+        tma_load_2d(dst, map, k, m0, bar(kMidFull + s));
+        if (kBK == 2 * kMidLine) tma_load_2d(dst + line_x, map, k + kMidLine, m0, bar(kMidFull + s));
       }
       __syncwarp();
       if (++kb == KB) {
         kb = 0;
         ++tile;
+        m0 = static_cast<int>((tile % a.p.tok_tiles) * T);
+      }
+      if (++s == stages) {
+        s = 0;
+        phase ^= 1;
       }
     }
     if (lane == 0) {  // own copies landed before leaving (complete on the normal path)
-      for (uint32_t n = 0; n < x_stages && n < pos; ++n) {
+      for (uint32_t n = 0; n < stages && n < pos; ++n) {
         const uint32_t j = pos - 1 - n;
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bar(kMidFullX + j % x_stages), (j / x_stages) & 1) &&
+        while (!mbar_try_wait(bar(kMidFull + j % stages), (j / stages) & 1) &&
                globaltimer() - t0 < kWaitLimitNs) {
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t fmt = F16 ? 0u : 1u;
-      constexpr bool kMN = MODE == kMidBackward;
-      const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (kMN ? 1u << 15 : 0u) |
-                             ((T >> 3) << 17) | (static_cast<uint32_t>(kMidRows >> 4) << 24);
-      uint32_t kb = first % KB, it = 0, seg = 0;
-      bool go = true;
-      for (uint32_t pos = 0; pos < count && go; ++pos) {
-        const uint32_t buf = seg % bufs;
-        const bool begins = pos == 0 || kb == 0;
-        if (begins && !mbar_wait(bar(kMidAccEmpty + buf), ((seg / bufs) & 1) ^ 1, abort_flag)) break;
-        const uint32_t sx = pos % x_stages;
-        if (!mbar_wait(bar(kMidFullX + sx), (pos / x_stages) & 1, abort_flag)) break;
-        const uint64_t dx = sw128_kmajor_desc(sbase + a.p.off_x + sx * x_bytes);
+    // The whole warp walks along, so that its counters and descriptors stay in uniform registers;
+    // an elected lane issues. This loop's latency paces small token counts: ring positions and
+    // phases are counted, not divided out, and a stage has one barrier each way.
+    constexpr uint32_t fmt = F16 ? 0u : 1u;
+    constexpr bool kMN = MODE == kMidBackward;
+    const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (kMN ? 1u << 15 : 0u) |
+                           ((T >> 3) << 17) | (static_cast<uint32_t>(kMidRows >> 4) << 24);
+    const uint64_t desc_w = kMN ? mid_mnmajor_desc(sbase) : sw128_kmajor_desc(sbase);
+    const uint64_t desc_x = sw128_kmajor_desc(sbase + 2 * kMidTileBytes);
+    const uint32_t issue = elect_one();
+    uint32_t kb = first % KB, s = 0, phase = 0, buf = 0, phase_acc = 1, pos = 0;
+    bool begins = true;
+    for (; pos < count; ++pos) {
+      bool go = !begins || mbar_wait(bar(kMidAccEmpty + buf), phase_acc, abort_flag);
+      go = go && mbar_wait(bar(kMidFull + s), phase, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, go)) break;
+      tc_fence_after();
+      const uint64_t at = static_cast<uint64_t>(s * (stage_bytes >> 4));
+      const uint32_t acc = tmem + buf * MATS * T;
 #pragma unroll
-        for (int m = 0; m < MATS; ++m, ++it) {
-          const uint32_t sw = it % kMidWStages;
-          if (!mbar_wait(bar(kMidFullW + sw), (it / kMidWStages) & 1, abort_flag)) {
-            go = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t wa = sbase + sw * kMidWBytes;
-          const uint64_t dw = kMN ? mid_mnmajor_desc(wa) : sw128_kmajor_desc(wa);
+      for (int h = 0; h < 2; ++h) {  // the stage's two W' tiles, 16 of the contraction at a time
+        const uint64_t dw = desc_w + at + h * (kMidTileBytes >> 4);
+        const uint64_t dx = desc_x + at + (MATS == 2 ? 0 : h * static_cast<uint64_t>(line_x >> 4));
 #pragma unroll
-          for (int k = 0; k < kMidBK / 16; ++k)
-            tc_mma(tmem + (buf * MATS + m) * T, dw + (kMN ? 128 : 2) * k, dx + 2 * k, idesc,
-                   !(begins && k == 0));
-          tc_commit(bar(kMidEmptyW + sw));
-        }
-        if (!go) break;
-        tc_commit(bar(kMidEmptyX + sx));
-        if (++kb == KB || pos + 1 == count) {
-          kb = kb == KB ? 0 : kb;
-          tc_commit(bar(kMidAccFull + buf));
-          ++seg;
+        for (int k = 0; k < kMidLine / 16; ++k)
+          tc_mma_one(MATS == 2 ? acc + h * T : acc, dw + (kMN ? 128 : 2) * k, dx + 2 * k, idesc,
+                     !begins || k != 0 || (MATS == 1 && h != 0), issue);
+      }
+      tc_commit_one(bar(kMidEmpty + s), issue);
+      begins = ++kb == KB;
+      if (begins) kb = 0;
+      if (++s == stages) {
+        s = 0;
+        phase ^= 1;
+      }
+      if (begins || pos + 1 == count) {
+        tc_commit_one(bar(kMidAccFull + buf), issue);
+        if (++buf == bufs) {
+          buf = 0;
+          phase_acc ^= 1;
         }
       }
-      // the issued MMAs have read their operands before the CTA leaves
-      for (uint32_t n = 0; n < kMidWStages && n < it; ++n) {
-        const uint32_t j = it - 1 - n;
+    }
+    if (lane == 0) {  // the issued MMAs have read their operands before the CTA leaves
+      for (uint32_t n = 0; n < stages && n < pos; ++n) {
+        const uint32_t j = pos - 1 - n;
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(bar(kMidEmptyW + j % kMidWStages), (j / kMidWStages) & 1) &&
+        while (!mbar_try_wait(bar(kMidEmpty + j % stages), (j / stages) & 1) &&
                globaltimer() - t0 < kWaitLimitNs) {
         }
       }
@@ -240,95 +254,118 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     const uint32_t group = (warp - 2) / 8, wi = (warp - 2) % 8;
     const uint32_t rows = static_cast<uint32_t>(a.rows), cols = static_cast<uint32_t>(a.cols);
     const uint32_t gpr = cols >> a.w.lg_group;
-    // the thread's row in the block of weight rows, and its 32 columns in the block of columns
-    const uint32_t r = MODE == kMidBackward ? 16 * (wi >> 1) + (lane >> 1) : 16 * wi + (lane >> 1);
-    const uint32_t cc = MODE == kMidBackward ? 64 * (wi & 1) + 32 * (lane & 1) : 32 * (lane & 1);
-    const uint32_t step = MATS == 2 ? 1 : 2;  // units from one of the group's tiles to its next
-    uint8_t* ring = smem + a.p.off_ring + (warp - 2) * (kDepth * kSlot) + lane * kPiece;
+    // The thread's row of the block of the weight, and which half of the columns: eight lanes in a row
+    // write eight different 16-byte pieces of the swizzled lines (no bank conflicts).
+    const uint32_t r = 16 * wi + (lane & 7) + 8 * (lane >> 4), half = (lane >> 3) & 1;
+    const uint32_t cc = (MATS == 2 ? 32 : 64) * half;
+    uint8_t* ring = smem + a.p.off_ring + (warp - 2) * (kDepth * 2 * kSlot) + lane * kPiece;
     const uint32_t ring_u = smem_u32(ring);
-    const uint32_t swz = (MODE == kMidBackward ? (wi & 1) * 8192u : 0u) + r * 128u;
+    // Where chunk h goes in a stage: line_at + h * line_h, pieces piece0 + h * piece_h ..
+    //   linear: the halves are the stage's two tiles, a thread's chunks one line of its tile;
+    //   gated: the weights are the two tiles, the halves the two halves of a line;
+    //   backward (MN-major): rows 64 .. are the second tile, the halves its two 8 KB blocks of 64
+    //   features, a thread's chunks one line.
+    const uint32_t line_at = MODE == kMidBackward ? (r >> 6) * kMidTileBytes + half * 8192u + (r & 63) * 128u
+                             : MATS == 2          ? r * 128u
+                                                  : half * kMidTileBytes + r * 128u;
+    const uint32_t line_h = MATS == 2 ? kMidTileBytes : 0u;
+    const uint32_t piece0 = MATS == 2 ? 4 * half : 0u;
+    constexpr uint32_t piece_h = MATS == 2 ? 0 : 4;
 
-    // Where a walk along the group's tiles stands: unit `pos` of the CTA, its tile and k-block.
+    // Where a walk along the group's stages stands: unit `pos` of the CTA, its tile and k-block, and the
+    // weight, first row and first column of its block.
     struct Walk {
-      uint32_t pos, tile, kb;
+      uint32_t pos, tile, kb, mat, row, col;
+    };
+    auto place = [&](Walk& w, bool new_tile) {
+      if (new_tile) {
+        const uint32_t block = w.tile / a.p.tok_tiles * kMidRows;
+        if constexpr (MODE == kMidBackward)
+          w.col = block;
+        else
+          w.row = block;
+      }
+      if constexpr (MODE == kMidBackward) {
+        w.mat = w.kb >= static_cast<uint32_t>(a.p.kb1) ? 1 : 0;
+        w.row = (w.kb - w.mat * a.p.kb1) * kBK;
+      } else {
+        w.col = w.kb * kBK;
+      }
     };
     auto start = [&]() {
       Walk w;
-      w.pos = MATS == 2 ? 0 : group;
-      w.tile = (first + w.pos) / KB;
-      w.kb = first + w.pos - w.tile * KB;
+      w.pos = group;
+      w.tile = (first + group) / KB;
+      w.kb = first + group - w.tile * KB;
+      w.mat = 0;
+      place(w, true);
       return w;
     };
-    auto advance = [&](Walk& w) {
-      const uint32_t tile = w.tile;
-      w.pos += step;
-      w.kb += step;
+    auto advance = [&](Walk& w) {  // to the group's next stage; whether that is another tile's
+      w.pos += 2;
+      w.kb += 2;
+      const bool other = w.kb >= KB;
       while (w.kb >= KB) {
         w.kb -= KB;
         ++w.tile;
       }
-      return w.tile != tile;
+      place(w, other);
+      return other;
     };
-    // The weight, first row and first column of a unit.
-    struct Place {
-      uint32_t mat, row, col;
-    };
-    auto place = [&](const Walk& w) {
-      const uint32_t block = w.tile / a.p.tok_tiles * kMidRows;
-      Place p;
-      if constexpr (MODE == kMidBackward) {
-        p.mat = w.kb >= static_cast<uint32_t>(a.p.kb1) ? 1 : 0;
-        p.row = (w.kb - p.mat * a.p.kb1) * kMidBK;
-        p.col = block;
-      } else {
-        p.mat = MATS == 2 ? group : 0;
-        p.row = block;
-        p.col = w.kb * kMidBK;
-      }
-      return p;
-    };
+    const uint32_t row_codes = r * cols + cc, row_meta = r * gpr;  // the thread's part of an offset
 
-    Walk cw = start(), mw = start(), w = start();
-    const uint8_t* copy_base = nullptr;
-    uint32_t copy_code0 = 0;
+    Walk cw = start(), mw = cw, w = cw;
+    // codes: the block's first byte (3 bits: word) in either weight of a stage
+    const uint8_t* copy_base[MATS];
+    uint32_t copy_code0[MATS];
     auto aim_copies = [&]() {
-      if (cw.pos < count) {
-        const Place p = place(cw);
-        const int64_t e0 = static_cast<int64_t>(p.row) * cols;
-        copy_base = a.w.packed[p.mat] + (NBITS == 3 ? e0 / 10 * 4 : e0 / 8 * NBITS);
-        copy_code0 = NBITS == 3 ? static_cast<uint32_t>(e0 % 10) : 0u;
+      const int64_t e0 = static_cast<int64_t>(cw.row) * cols;
+#pragma unroll
+      for (int i = 0; i < MATS; ++i) {
+        copy_base[i] = a.w.packed[MATS == 2 ? i : cw.mat] + (NBITS == 3 ? e0 / 10 * 4 : e0 / 8 * NBITS);
+        copy_code0[i] = NBITS == 3 ? static_cast<uint32_t>(e0 % 10) : 0u;
       }
     };
     auto copy_next = [&](uint32_t slot) {
       if (cw.pos < count) {
-        const Place p = place(cw);
-        const uint32_t col = p.col + cc;
-        if (p.row + r < rows && col < cols) {
-          const uint32_t e = r * cols + col;
-          if constexpr (NBITS == 3)
-            copy_chunk<NBITS>(ring_u + slot * kSlot, copy_base, copy_code0 + e);
-          else
-            copy_chunk<NBITS>(ring_u + slot * kSlot, copy_base, e / 8 * NBITS);
+        const uint32_t col = cw.col + cc, e = row_codes + cw.col;
+        if (cw.row + r < rows) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t more = MATS == 2 ? 0 : 32 * h;
+            if (col + more >= cols) break;
+            const uint32_t to = ring_u + (slot * 2 + h) * kSlot;
+            const int i = MATS == 2 ? h : 0;
+            if constexpr (NBITS == 3)
+              copy_chunk<NBITS>(to, copy_base[i], copy_code0[i] + e + more);
+            else
+              copy_chunk<NBITS>(to, copy_base[i], (e + more) / 32 * (4 * NBITS));
+          }
         }
         if (advance(cw) || MODE == kMidBackward) aim_copies();
       }
       cp_async_commit();
     };
-    Slab slab;
-    RawMeta<ANY> next[kGroups];
+    // scale and zero of the two chunks
+    constexpr int kMeta = kShared ? 1 : 2;
+    Slab slab[MATS];
+    RawMeta<ANY> next[kMeta][kGroups];
     auto aim = [&]() {
-      const Place p = place(mw);
-      slab = slab_of_row<NBITS, ANY>(a.w, p.mat, p.row, cols, gpr);
+#pragma unroll
+      for (int i = 0; i < MATS; ++i)
+        slab[i] = slab_of_row<NBITS, ANY>(a.w, MATS == 2 ? i : mw.mat, mw.row, cols, gpr);
     };
     auto fetch_meta = [&]() {
-      if (mw.pos >= count) return;
-      const Place p = place(mw);
-      const uint32_t col = p.col + cc;
-      if (p.row + r >= rows) return;
+      const uint32_t col = mw.col + cc;
+      if (mw.pos >= count || mw.row + r >= rows) return;
 #pragma unroll
-      for (int u = 0; u < kGroups; ++u) {
-        if (col + GROUP * u >= cols) break;
-        next[u] = load_raw_meta<ANY>(slab, a.w, 0u, r * gpr + ((col + GROUP * u) >> a.w.lg_group));
+      for (int h = 0; h < kMeta; ++h) {
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+          const uint32_t at = col + (MATS == 2 ? 0 : 32 * h) + GROUP * u;
+          if (at < cols)
+            next[h][u] = load_raw_meta<ANY>(slab[MATS == 2 ? h : 0], a.w, 0u, row_meta + (at >> a.w.lg_group));
+        }
       }
     };
     if (w.pos < count) {
@@ -340,62 +377,84 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         for (uint32_t s = 0; s < kDepth; ++s) copy_next(s);
       }
     }
-    uint32_t slot = 0;
+    uint32_t slot = 0, s = group % stages, phase = group >= stages ? 0 : 1;
     for (; w.pos < count; advance(w)) {
-      const uint32_t it = MATS == 2 ? 2 * w.pos + group : w.pos;
-      const Place p = place(w);
-      const uint32_t col = p.col + cc;
-      const bool in = p.row + r < rows && col < cols;
-      Codes32<NBITS> c;
-      GroupMeta m[kGroups];
-      bool one = !ANY;
+      const uint32_t col = w.col + cc;
+      const bool in_row = w.row + r < rows;
       if constexpr (kWhole) {
+        GroupMeta m[kMeta][kGroups];
+        bool one = !ANY;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
-          float2 sz = meta_f32_pair<ANY, F16>(next[u], slab, a.w.meta_dt);
-          if (!in) sz = make_float2(0.0f, 0.0f);  // W' = 0 outside the weight
-          m[u] = group_meta<NBITS>(sz.x, sz.y, &one);
-        }
-        const uint32_t off = slab.code0 + r * cols + col;
-        if (advance(mw) || MODE == kMidBackward) {
-          if (mw.pos < count) aim();
-        }
+        for (int h = 0; h < kMeta; ++h)
+#pragma unroll
+          for (int u = 0; u < kGroups; ++u) {
+            float2 sz = meta_f32_pair<ANY, F16>(next[h][u], slab[MATS == 2 ? h : 0], a.w.meta_dt);
+            // W' = 0 outside the weight
+            if (!in_row || col + (MATS == 2 ? 0 : 32 * h) + GROUP * u >= cols) sz = make_float2(0.0f, 0.0f);
+            m[h][u] = group_meta<NBITS>(sz.x, sz.y, &one);
+          }
+        one = !ANY && __all_sync(0xFFFFFFFFu, one);
+        uint32_t off[MATS];
+#pragma unroll
+        for (int i = 0; i < MATS; ++i) off[i] = slab[i].code0 + row_codes + w.col;
+        if ((advance(mw) || MODE == kMidBackward) && mw.pos < count) aim();
         fetch_meta();
         cp_async_wait<kDepth - 1>();  // the thread's own copies: no other reads them
-        c = read_chunk<NBITS>(ring + slot * kSlot, off);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(kMidEmpty + s), phase, abort_flag))) break;
+        uint8_t* to = smem + s * stage_bytes + line_at;
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+          const Codes32<NBITS> c = read_chunk<NBITS>(ring + (slot * 2 + h) * kSlot,
+                                                     MATS == 2 ? off[h] : off[0] + 32 * h);
+          uint4 o[4];
+          if (one)
+            dequant_chunk<NBITS, OUT, kGroups, true>(c, m[kShared ? 0 : h], o);
+          else
+            dequant_chunk<NBITS, OUT, kGroups, false>(c, m[kShared ? 0 : h], o);
+#pragma unroll
+          for (uint32_t u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(to + h * line_h + (((piece0 + h * piece_h + u) ^ (r & 7)) << 4)) = o[u];
+        }
       } else {
-        const uint32_t left = in ? min(4u, (cols - col) / 8) : 0u;
         if (w.pos != mw.pos) {
           mw = w;
           aim();
         }
-        c = load_codes_units<NBITS>(slab.codes, slab.code0 + r * cols + col, static_cast<int>(left));
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(kMidEmpty + s), phase, abort_flag))) break;
+        uint8_t* to = smem + s * stage_bytes + line_at;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
-          float2 sz = make_float2(0.0f, 0.0f);
-          if (static_cast<uint32_t>(u) < left)
-            sz = meta_f32_pair<ANY, F16>(
-                load_raw_meta<ANY>(slab, a.w, 0u, r * gpr + ((col + 8 * u) >> a.w.lg_group)), slab,
-                a.w.meta_dt);
-          m[u] = group_meta<NBITS>(sz.x, sz.y, &one);
+        for (uint32_t h = 0; h < 2; ++h) {
+          const Slab& b = slab[MATS == 2 ? h : 0];
+          const uint32_t more = MATS == 2 ? 0 : 32 * h, at = col + more;
+          const uint32_t left = in_row && at < cols ? min(4u, (cols - at) / 8) : 0u;
+          const Codes32<NBITS> c = load_codes_units<NBITS>(b.codes, b.code0 + row_codes + w.col + more,
+                                                           static_cast<int>(left));
+          GroupMeta m[4];
+          bool one = false;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float2 sz = make_float2(0.0f, 0.0f);
+            if (static_cast<uint32_t>(u) < left)
+              sz = meta_f32_pair<ANY, F16>(
+                  load_raw_meta<ANY>(b, a.w, 0u, row_meta + ((at + 8 * u) >> a.w.lg_group)), b,
+                  a.w.meta_dt);
+            m[u] = group_meta<NBITS>(sz.x, sz.y, &one);
+          }
+          uint4 o[4];
+          dequant_chunk<NBITS, OUT, 4, false>(c, m, o);
+#pragma unroll
+          for (uint32_t u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(to + h * line_h + (((piece0 + h * piece_h + u) ^ (r & 7)) << 4)) = o[u];
         }
       }
-      uint4 o[4];
-      if (!ANY && __all_sync(0xFFFFFFFFu, one))
-        dequant_chunk<NBITS, OUT, kGroups, true>(c, m, o);
-      else
-        dequant_chunk<NBITS, OUT, kGroups, false>(c, m, o);
-      const uint32_t sw = it % kMidWStages;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(kMidEmptyW + sw), ((it / kMidWStages) & 1) ^ 1,
-                                             abort_flag)))
-        break;
-      uint8_t* tile = smem + sw * kMidWBytes + swz;
-#pragma unroll
-      for (uint32_t u = 0; u < 4; ++u)
-        *reinterpret_cast<uint4*>(tile + (((4 * (lane & 1) + u) ^ (r & 7)) << 4)) = o[u];
       fence_proxy_async_smem();  // generic-proxy writes -> read by the tensor core
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kMidFullW + sw));
+      if (lane == 0) mbar_arrive(bar(kMidFull + s));
+      s += 2;  // the other group fills the stage between
+      while (s >= stages) {
+        s -= stages;
+        phase ^= 1;
+      }
       if constexpr (kWhole) {
         copy_next(slot);
         slot = slot + 1 == kDepth ? 0 : slot + 1;
@@ -455,7 +514,8 @@ __global__ void __launch_bounds__(kMidThreads, 1)
 }
 
 // Tiles that several CTAs share: their partial tiles added in the order of k, then the epilogue.
-// A block takes 8 tokens of a tile.
+// A block takes 32 tokens of a tile, a lane 4 outputs of a token at a time. Launched while the
+// product runs (programmatic dependent launch): it waits for its end first.
 template <bool F16, int MATS>
 __global__ void __launch_bounds__(256) mid_finish_kernel(const MidArgs a) {
   const uint32_t T = static_cast<uint32_t>(a.p.tok), KB = static_cast<uint32_t>(a.p.kb);
@@ -464,22 +524,35 @@ __global__ void __launch_bounds__(256) mid_finish_kernel(const MidArgs a) {
   const uint32_t tile = blockIdx.x;
   const uint32_t c0 = mid_cta_of(tile * KB, ctas, units);
   const uint32_t c1 = mid_cta_of(tile * KB + KB - 1, ctas, units);
-  if (c0 == c1) return;  // one CTA had it whole
-  const uint32_t row = threadIdx.x & 127;
+  // c0 may have begun with an earlier tile (then this one is its last); the others begin with this
+  const uint32_t slot0 = 2 * c0 + (mid_first_unit(c0, ctas, units) / KB != tile ? 1 : 0);
+  const uint32_t row = (threadIdx.x & 31) * 4;
   const int n = static_cast<int>(tile / a.p.tok_tiles * kMidRows + row);
-  if (n >= a.out) return;
   const int64_t tok0 = static_cast<int64_t>(tile % a.p.tok_tiles) * T;
-  for (uint32_t i = threadIdx.x >> 7; i < 8; i += 2) {
-    const uint32_t t = blockIdx.y * 8 + i;
-    if (t >= T || tok0 + t >= a.M) return;
-    float s[2] = {0.0f, 0.0f};
-    for (uint32_t c = c0; c <= c1; ++c) {
-      const uint32_t second = mid_first_unit(c, ctas, units) / KB != tile ? 1 : 0;
-      const float* part = a.partial + static_cast<size_t>(2 * c + second) * MATS * T * kMidRows + row;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1 || n >= a.out) return;
+  const size_t slot = static_cast<size_t>(MATS) * T * kMidRows;
+  const uint32_t end = min(T, (blockIdx.y + 1) * 32);
+  for (uint32_t t = blockIdx.y * 32 + (threadIdx.x >> 5); t < end; t += 8) {
+    if (tok0 + t >= a.M) return;
+    float s[MATS][4];
 #pragma unroll
-      for (int m = 0; m < MATS; ++m) s[m] = __fadd_rn(s[m], part[(m * T + t) * kMidRows]);
+    for (int m = 0; m < MATS; ++m) {
+      const float* part = a.partial + (static_cast<size_t>(m) * T + t) * kMidRows + row;
+      float4 v = __ldcg(reinterpret_cast<const float4*>(part + slot0 * slot));
+      for (uint32_t c = c0 + 1; c <= c1; ++c) {
+        const float4 p = __ldcg(reinterpret_cast<const float4*>(part + 2 * c * slot));
+        v = make_float4(__fadd_rn(v.x, p.x), __fadd_rn(v.y, p.y), __fadd_rn(v.z, p.z),
+                        __fadd_rn(v.w, p.w));
+      }
+      s[m][0] = v.x;
+      s[m][1] = v.y;
+      s[m][2] = v.z;
+      s[m][3] = v.w;
     }
-    mid_store<F16, MATS>(a, tok0 + t, n, s[0], s[1]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      mid_store<F16, MATS>(a, tok0 + t, n + q, s[0][q], MATS == 2 ? s[MATS - 1][q] : 0.0f);
   }
 }
 
@@ -492,7 +565,7 @@ cudaError_t launch_mid_mode(const MidJob& j, const MidPlan& plan, cudaStream_t s
   CUtensorMap x[2];
   for (int i = 0; i < 2; ++i) {
     const void* p = MODE == kMidBackward && j.weights == 2 ? j.X[i] : j.X[0];
-    if (!make_map(&x[i], dt, 2, p, inner, j.M, kMidBK, static_cast<uint32_t>(plan.tok),
+    if (!make_map(&x[i], dt, 2, p, inner, j.M, 64, static_cast<uint32_t>(plan.tok),
                   CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
@@ -511,7 +584,10 @@ cudaError_t launch_mid_mode(const MidJob& j, const MidPlan& plan, cudaStream_t s
   a.p = plan;
   const bool any = any_meta(j.w, j.weights, j.meta_dtype, j.x_dtype), whole = j.cols % 32 == 0;
   auto kernel = mid_tokens_kernel<NBITS, F16, MODE, 8, true>;
-  if (j.group_size >= 32)
+  if (j.group_size >= 64)
+    kernel = any ? mid_tokens_kernel<NBITS, F16, MODE, 64, true>
+                 : mid_tokens_kernel<NBITS, F16, MODE, 64, false>;
+  else if (j.group_size == 32)
     kernel = any ? mid_tokens_kernel<NBITS, F16, MODE, 32, true>
                  : mid_tokens_kernel<NBITS, F16, MODE, 32, false>;
   else if (whole && j.group_size == 16 && !any)
@@ -522,10 +598,17 @@ cudaError_t launch_mid_mode(const MidJob& j, const MidPlan& plan, cudaStream_t s
   kernel<<<plan.ctas, kMidThreads, plan.smem, st>>>(x[0], x[1], a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (plan.row_tiles * plan.tok_tiles % plan.ctas == 0) return cudaSuccess;  // no tile is shared
-  const dim3 grid(static_cast<unsigned>(plan.row_tiles * plan.tok_tiles),
-                  static_cast<unsigned>((plan.tok + 7) / 8));
-  mid_finish_kernel<F16, MODE == kMidGated ? 2 : 1><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.row_tiles * plan.tok_tiles),
+                     static_cast<unsigned>((plan.tok + 31) / 32));
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, mid_finish_kernel<F16, MODE == kMidGated ? 2 : 1>, a);
 }
 
 }  // namespace
