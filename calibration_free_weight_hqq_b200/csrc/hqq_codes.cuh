@@ -164,12 +164,12 @@ __device__ __forceinline__ void dequant_chunk(const Codes32<NBITS>& c, const Gro
   }
 }
 
-// Copies through L1: a lane's 32 contiguous bytes are one sector in two pieces, and bypassing L1 would
-// fetch it twice (28672 x 4096, one token: 32 -> 28 us).
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
-               : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -179,65 +179,107 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Copies a lane's 32 codes into its own shared-memory slot: from byte `off` of `base` on or, at
-// 3 bits, from element `off` on counted from the first code of the word at `base`. Row lengths are
-// multiples of 32 codes, so every copy is aligned to its width. A slot's pieces lie 32 lanes apart, so
-// that a warp's pieces are contiguous. `slot` points at the lane's first piece.
-template <int NBITS>
-__device__ __forceinline__ void copy_chunk(uint32_t slot, const uint8_t* base, uint32_t off) {
-  if constexpr (NBITS == 3) {
-    const uint32_t word = off / 10u, first = off - word * 10u;
-    const uint8_t* p = base + word * 4u;
-#pragma unroll
-    for (int i = 0; i < 5; ++i)  // 31 codes further: the fifth word only from slot 9
-      if (i < 4 || first == 9u) cp_async<4>(slot + i * 128, p + 4 * i);
-  } else {
-    constexpr int kPiece = NBITS >= 4 ? 16 : 4 * NBITS;
-#pragma unroll
-    for (int i = 0; i < 4 * NBITS / kPiece; ++i)
-      cp_async<kPiece>(slot + i * 32 * kPiece, base + off + i * kPiece);
+// A warp's tile of 16 rows x CODES consecutive codes in shared memory, copied by the warp together:
+// neighbouring lanes take neighbouring 16-byte pieces of a row. (Each lane copying its own 32 codes
+// touched a sector or two per lane and filled the L1's data path: 32 wavefronts a copy.) The pieces
+// of a row are permuted by its number so that reads are free of bank conflicts, for eight lanes that
+// read the same piece of eight rows (QUADS false) or chunks 0, 2, 4, 6 of two rows (QUADS true).
+// Except at 3 bits, rows must start on 16-byte boundaries.
+template <int NBITS, int CODES, bool QUADS>
+struct CodeTile {
+  static constexpr int kRow = tile_row_bytes(NBITS, CODES);
+  static constexpr int kPiece = kRow < 16 ? kRow : 16;  // not at 3 bits
+  static constexpr int kPieces = kRow / kPiece;
+
+  static __device__ __forceinline__ uint32_t place(uint32_t row, uint32_t piece) {
+    if constexpr (QUADS && kPieces == 16) return piece ^ ((piece >> 3) & 1) ^ ((row & 1) << 1);
+    if constexpr (QUADS) return kPieces == 8 ? piece ^ (row & 1) : piece;
+    if constexpr (kPieces > 1) return piece ^ ((row / (8 / kPieces)) & (kPieces - 1));
+    return piece;
   }
+
+  // The first `rows` rows and `codes` codes of each. src: the first code's byte, rows `stride` bytes
+  // apart; at 3 bits the word from which `first` counts the first code, rows `stride` codes apart.
+  static __device__ __forceinline__ void copy(uint32_t to, const uint8_t* src, uint32_t first,
+                                              uint32_t stride, uint32_t rows, uint32_t codes,
+                                              uint32_t lane) {
+    if constexpr (NBITS == 3) {
+      constexpr uint32_t kWords = kRow / 4;
+#pragma unroll 4
+      for (uint32_t i = lane; i < 16 * kWords; i += 32) {
+        const uint32_t row = i / kWords, word = i - row * kWords;
+        const uint32_t e = first + row * stride, w0 = e / 10u;
+        if (row < rows && 10u * word <= e - 10u * w0 + codes - 1)  // a code of the row is in the word
+          cp_async<4>(to + i * 4, src + (w0 + word) * 4u);
+      }
+    } else {
+      constexpr uint32_t kAll = 16 * kPieces;
+#pragma unroll
+      for (uint32_t n = 0; n < (kAll + 31) / 32; ++n) {
+        const uint32_t i = n * 32 + lane, row = i / kPieces, piece = i % kPieces;
+        if (i < kAll && row < rows && piece * (kPiece * 8 / NBITS) < codes)
+          cp_async<kPiece>(to + row * kRow + place(row, piece) * kPiece,
+                           src + row * stride + piece * kPiece);
+      }
+    }
+  }
+
+  // The 32 codes of `row` from code `at` (a multiple of 32) on; at 3 bits, slot: the first code of
+  // the row's place in its word.
+  static __device__ __forceinline__ Codes32<NBITS> read(const uint8_t* tile, uint32_t row, uint32_t at,
+                                                        uint32_t slot) {
+    Codes32<NBITS> c;
+    if constexpr (NBITS == 3) {
+      const uint32_t word = (slot + at) / 10u;
+      const int first_slot = static_cast<int>(slot + at - 10u * word);
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + row * kRow) + word;
+      uint32_t v[5];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = p[i];
+      v[4] = first_slot == 9 ? p[4] : 0u;  // 31 codes further: the fifth word only from slot 9
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int here = first_slot + 8 * u;  // 8u .. 8u + 9
+        const int word0 = 8 * u / 10;         // the word of code 8u, or the next one
+        const bool next = here >= 10 * (word0 + 1);
+        const int s = here - 10 * (word0 + (next ? 1 : 0));
+        const uint32_t lo = next ? v[word0 + 1] : v[word0];
+        const uint32_t hi = next ? v[word0 + 2 < 5 ? word0 + 2 : 4] : v[word0 + 1];
+        c.w[u] = (lo & 0x3FFFFFFFu) >> (3 * s) | hi << (30 - 3 * s);
+      }
+    } else {
+      const uint32_t byte = at / 8 * NBITS;
+      const uint8_t* line = tile + row * kRow;
+      if constexpr (NBITS >= 4) {
+#pragma unroll
+        for (int i = 0; i < NBITS / 4; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(line + place(row, byte / 16 + i) * 16);
+          c.w[4 * i] = v.x;
+          c.w[4 * i + 1] = v.y;
+          c.w[4 * i + 2] = v.z;
+          c.w[4 * i + 3] = v.w;
+        }
+      } else {
+        const uint8_t* p = line + place(row, byte / kPiece) * kPiece + byte % kPiece;
+        if constexpr (NBITS == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          c.w[0] = v.x;
+          c.w[1] = v.y;
+        } else {
+          c.w[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+      }
+    }
+    return c;
+  }
+};
+
+// Whether rows of `cols` codes can be copied as CodeTile wants them.
+inline bool whole_rows(int nbits, int64_t cols) {
+  return cols % 32 == 0 && (nbits == 3 || cols / 8 * nbits % 16 == 0);
 }
 
-// The chunk in a lane's slot (3 bits: `off` as it was copied).
-template <int NBITS>
-__device__ __forceinline__ Codes32<NBITS> read_chunk(const uint8_t* slot, uint32_t off) {
-  Codes32<NBITS> c;
-  if constexpr (NBITS == 3) {
-    uint32_t v[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] = *reinterpret_cast<const uint32_t*>(slot + 128 * i);
-    const int first_slot = static_cast<int>(off % 10u);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int at = first_slot + 8 * u;      // 8u .. 8u + 9
-      const int first = 8 * u / 10;           // the word of code 8u, or the next one
-      const bool next = at >= 10 * (first + 1);
-      const int s = at - 10 * (first + (next ? 1 : 0));
-      const uint32_t lo = next ? v[first + 1] : v[first];
-      const uint32_t hi = next ? v[first + 2 < 5 ? first + 2 : 4] : v[first + 1];
-      c.w[u] = (lo & 0x3FFFFFFFu) >> (3 * s) | hi << (30 - 3 * s);
-    }
-  } else if constexpr (NBITS >= 4) {
-#pragma unroll
-    for (int i = 0; i < NBITS / 4; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(slot + 512 * i);
-      c.w[4 * i] = v.x;
-      c.w[4 * i + 1] = v.y;
-      c.w[4 * i + 2] = v.z;
-      c.w[4 * i + 3] = v.w;
-    }
-  } else if constexpr (NBITS == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(slot);
-    c.w[0] = v.x;
-    c.w[1] = v.y;
-  } else {
-    c.w[0] = *reinterpret_cast<const uint32_t*>(slot);
-  }
-  return c;
-}
-
-// As above for rows of any multiple of 8 codes, in units of 8 codes (NBITS bytes, aligned to their
+// A lane's chunk straight from memory, for rows of any multiple of 8 codes, in units of 8 codes (NBITS bytes, aligned to their
 // size): the first `units` of the chunk exist, the others read as code 0.
 template <int NBITS>
 __device__ __forceinline__ Codes32<NBITS> load_codes_units(const uint8_t* slab, uint32_t e,
@@ -276,7 +318,7 @@ __device__ __forceinline__ Codes32<NBITS> load_codes_units(const uint8_t* slab, 
 
 // Consecutive rows of one weight: their codes and meta, addressed by 32-bit offsets from here.
 struct Slab {
-  const uint8_t* codes;   // see copy_chunk
+  const uint8_t* codes;   // the first code's byte; at 3 bits the word that holds it
   const uint8_t *scale, *zero;
   const float2 *scale_mm, *zero_mm;  // from the run of the slab's first group on, or nullptr
   uint32_t code0;         // 3 bits: slot of the slab's first code in its word

@@ -22,7 +22,7 @@ constexpr int kFewRed = 8 * kFewRedStride * 4;  // bytes of one warp's partial t
 // k-blocks whose codes are in flight per warp: about 6 KB of them, 96 KB an SM at 16 warps (the
 // memory's latency at full bandwidth asks for about 40), but 1 at least and 4 at most.
 __host__ __device__ constexpr int few_depth(int nbits, int mats) {
-  const int n = 6144 / (128 * mats * chunk_bytes(nbits));
+  const int n = 6144 / (mats * tile_bytes(nbits, kFewKB));
   return n < 1 ? 1 : n > 4 ? 4 : n;
 }
 // Bytes of a token's row of X in shared memory (padded by 64).
@@ -33,7 +33,7 @@ __host__ __device__ constexpr uint32_t few_x_row(uint32_t K) {
 __host__ __device__ constexpr size_t few_smem(int nbits, int mats, int warps, int64_t M, int64_t K) {
   return static_cast<size_t>(M) * few_x_row(static_cast<uint32_t>(K)) +
          static_cast<size_t>(warps * mats) *
-             (kFewRed + few_depth(nbits, mats) * 4 * 32 * chunk_bytes(nbits));
+             (kFewRed + few_depth(nbits, mats) * tile_bytes(nbits, kFewKB));
 }
 
 // Warps of a CTA: 8 with two CTAs an SM where their X fits in half the shared memory (a CTA's

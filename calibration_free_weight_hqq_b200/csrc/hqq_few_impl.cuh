@@ -16,8 +16,8 @@
 //     warp's reads are free of bank conflicts. CTAs are persistent over tiles of 16 rows.
 //   * The warps of a CTA split K, k-block by k-block in turn; their partial sums meet in shared
 //     memory and are added in warp order (deterministic).
-//   * Codes come by asynchronous copies several k-blocks ahead (across tiles too), each lane into
-//     its own slots (no barrier); scale and zero one k-block ahead in registers.
+//   * Codes come by asynchronous copies a few k-blocks ahead (across tiles too), each warp its own;
+//     scale and zero one k-block ahead in registers.
 //   * Lanes without a token of their own (g >= M) repeat the last one; those results are dropped.
 #pragma once
 
@@ -98,8 +98,8 @@ __device__ __forceinline__ void stage_x(uint4* xs, const uint8_t* X, uint32_t M,
   }
 }
 
-// GROUP: 64 (groups of 64 codes or more), 32, 16 (K a multiple of 32 with both) or 8 (any group size
-// and K; codes and meta read where they are used). ANY: see RawMeta.
+// GROUP: 64 (groups of 64 codes or more), 32, 16 (whole_rows) or 8 (any group size and K; codes and
+// meta read where they are used). ANY: see RawMeta.
 template <int NBITS, bool F16, int MATS, int GROUP, bool ANY>
 __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const FewArgs a) {
   constexpr int OUT = F16 ? kF16 : kBF16;
@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
   constexpr int kGroups = 64 / GROUP;            // groups of a lane's codes of a k-block
   constexpr int kGroupsHalf = kGroups > 1 ? kGroups / 2 : 1;
   constexpr int kDepth = few_depth(NBITS, MATS);
-  constexpr int kSlot = 32 * chunk_bytes(NBITS);   // a warp's chunks of 8 rows
-  constexpr int kPiece = NBITS == 3 ? 4 : NBITS >= 4 ? 16 : 4 * NBITS;
+  using Tile = CodeTile<NBITS, kFewKB, true>;
+  constexpr int kTile = tile_bytes(NBITS, kFewKB);  // a warp's k-block
   extern __shared__ __align__(16) uint8_t smem[];
   // the shuffle tells the compiler that a warp's index, and all that follows from it, is uniform
   const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
@@ -120,8 +120,7 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
   uint4* xs = reinterpret_cast<uint4*>(smem);
   uint8_t* after_x = smem + static_cast<size_t>(a.M) * few_x_row(K);
   float* red = reinterpret_cast<float*>(after_x);  // [MATS][warps][8][kFewRedStride]
-  uint8_t* ring = after_x + MATS * warps * kFewRed + warp * (kDepth * 2 * MATS * 2 * kSlot) +
-                  lane * kPiece;
+  uint8_t* ring = after_x + MATS * warps * kFewRed + warp * (kDepth * MATS * kTile);
   const uint32_t ring_u = smem_u32(ring);
 
   // Rows g and g + 8 of a tile. N is a multiple of 8: rows 8 .. 15 all exist or none does, and where
@@ -133,17 +132,12 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
     return slab_of_row<NBITS, ANY>(a.w, i, static_cast<int64_t>(tile) * kFewRows, K, groups_per_row);
   };
 
-  // --- codes, kDepth k-blocks ahead: (copy_tile, copy_kb) is the next to ask for. A lane's place in
-  // a tile (copy_at) and a k-block's (uniform) add up to its address.
+  // --- codes, kDepth k-blocks ahead: (copy_tile, copy_kb) is the next to ask for
   constexpr uint32_t kStepCodes = NBITS == 3 ? kFewKB : kFewKB / 8 * NBITS;
-  auto lane_codes = [&](uint32_t row) {
-    const uint32_t e = row * K + 64 * t;
-    return NBITS == 3 ? e : e / 8 * NBITS;
-  };
+  const uint32_t row_step = NBITS == 3 ? K : K / 8 * NBITS;
   uint32_t copy_tile = warp < KB ? blockIdx.x : tiles, copy_kb = warp;
   const uint8_t* copy_base[MATS];
   uint32_t copy_code0[MATS];
-  uint32_t copy_at[2] = {lane_codes(g), 0};
   auto aim_copies = [&]() {
     if (copy_tile < tiles) {
 #pragma unroll
@@ -152,45 +146,32 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
         copy_base[i] = b.codes;
         copy_code0[i] = b.code0;
       }
-      copy_at[1] = lane_codes(second_row(copy_tile));
     }
   };
-  auto copy_half = [&](uint32_t st, int h) {
+  auto copy_next = [&](uint32_t st) {
     if (copy_tile < tiles) {
-      // a whole k-block, or the lane's chunk of a partial one
-      if ((copy_kb + 1) * kFewKB <= K || copy_kb * kFewKB + 64 * t + 32 * h < K) {
+      const uint32_t rows = min(static_cast<uint32_t>(kFewRows),
+                                static_cast<uint32_t>(a.N) - copy_tile * kFewRows);
+      const uint32_t codes = min(static_cast<uint32_t>(kFewKB), K - copy_kb * kFewKB);
 #pragma unroll
-        for (int i = 0; i < MATS; ++i) {
-          const uint32_t step = copy_kb * kStepCodes + h * (kStepCodes / 8);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t slot = ring_u + (((st * 2 + h) * MATS + i) * 2 + r) * kSlot;
-            if constexpr (NBITS == 3)
-              copy_chunk<NBITS>(slot, copy_base[i], copy_code0[i] + step + copy_at[r]);
-            else
-              copy_chunk<NBITS>(slot, copy_base[i] + step, copy_at[r]);
-          }
-        }
+      for (int i = 0; i < MATS; ++i) {
+        const uint32_t to = ring_u + (st * MATS + i) * kTile, step = copy_kb * kStepCodes;
+        Tile::copy(to, copy_base[i] + (NBITS == 3 ? 0u : step), copy_code0[i] + step, row_step, rows,
+                   codes, lane);
+      }
+      copy_kb += warps;
+      if (copy_kb >= KB) {
+        copy_kb = warp;
+        copy_tile += gridDim.x;
+        aim_copies();
       }
     }
     cp_async_commit();
   };
-  auto next_copy = [&]() {
-    copy_kb += warps;
-    if (copy_kb >= KB && copy_tile < tiles) {
-      copy_kb = warp;
-      copy_tile += gridDim.x;
-      aim_copies();
-    }
-  };
   if constexpr (kWhole) {
     aim_copies();
 #pragma unroll 1
-    for (uint32_t s = 0; s < kDepth; ++s) {
-      copy_half(s, 0);
-      copy_half(s, 1);
-      next_copy();
-    }
+    for (uint32_t s = 0; s < kDepth; ++s) copy_next(s);
   }
 
   stage_x<NBITS>(xs, a.X, static_cast<uint32_t>(a.M), K, KB);
@@ -255,11 +236,14 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
               m[i][r][u] = group_meta<NBITS>(sz.x, sz.y, &one);
             }
         one = !ANY && __all_sync(0xFFFFFFFFu, one);
-        uint32_t off[MATS][2];  // 3 bits: where the chunks start in their words
+        uint32_t slot[MATS][2];  // 3 bits: the first code's place in its word, of both rows
 #pragma unroll
         for (int i = 0; i < MATS; ++i) {
-          off[i][0] = slab[i].code0 + g * K + kb * kFewKB + 64 * t;
-          off[i][1] = slab[i].code0 + row1 * K + kb * kFewKB + 64 * t;
+          slot[i][0] = slot[i][1] = 0u;
+          if constexpr (NBITS == 3) {
+            slot[i][0] = (slab[i].code0 + g * K + kb * kFewKB) % 10u;
+            slot[i][1] = (slab[i].code0 + (g + 8) * K + kb * kFewKB) % 10u;
+          }
         }
         // the next k-block's meta, of the next tile after this one's last
         if (kb + warps < KB) {
@@ -268,16 +252,17 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
           aim(tile + gridDim.x);
           fetch_meta(warp);
         }
-        const uint8_t* slots = ring + st * (2 * MATS * 2 * kSlot);
+        const uint8_t* block = ring + st * (MATS * kTile);
+        cp_async_wait<kDepth - 1>();
+        __syncwarp();  // every lane's copies have landed
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          cp_async_wait<2 * kDepth - 1>();  // the lane's own copies: no other thread reads them
 #pragma unroll
           for (int i = 0; i < MATS; ++i) {
             Codes32<NBITS> c[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              c[r] = read_chunk<NBITS>(slots + ((h * MATS + i) * 2 + r) * kSlot, off[i][r] + 32 * h);
+              c[r] = Tile::read(block + i * kTile, g + 8 * r, 64 * t + 32 * h, slot[i][r]);
             const GroupMeta* m0 = m[i][0] + (kGroups > 1 ? h * kGroupsHalf : 0);
             const GroupMeta* m1 = m[i][1] + (kGroups > 1 ? h * kGroupsHalf : 0);
             if (one)
@@ -285,9 +270,9 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
             else
               multiply_chunk<NBITS, F16, kGroupsHalf, false>(acc[i], c, m0, m1, x + 16 * h);
           }
-          copy_half(st, h);  // into the slots just read
         }
-        next_copy();
+        __syncwarp();  // every lane has read them
+        copy_next(st);
         st = st + 1 == kDepth ? 0 : st + 1;
       } else {
 #pragma unroll 1
@@ -369,16 +354,17 @@ cudaError_t launch_few_typed(const FewJob& j, const FewArgs& a, cudaStream_t st)
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, kSms * (16 / warps)));
   const size_t smem = few_smem(NBITS, MATS, warps, j.M, j.K);
   const bool any = any_meta(j.w, j.mats, j.meta_dtype, j.x_dtype);
-  const bool whole = j.K % 32 == 0;
   auto kernel = few_tokens_kernel<NBITS, F16, MATS, 8, true>;
-  if (j.group_size >= 64)
-    kernel = any ? few_tokens_kernel<NBITS, F16, MATS, 64, true>
-                 : few_tokens_kernel<NBITS, F16, MATS, 64, false>;
-  else if (j.group_size == 32)
-    kernel = any ? few_tokens_kernel<NBITS, F16, MATS, 32, true>
-                 : few_tokens_kernel<NBITS, F16, MATS, 32, false>;
-  else if (whole && j.group_size == 16 && !any)
-    kernel = few_tokens_kernel<NBITS, F16, MATS, 16, false>;
+  if (whole_rows(NBITS, j.K)) {
+    if (j.group_size >= 64)
+      kernel = any ? few_tokens_kernel<NBITS, F16, MATS, 64, true>
+                   : few_tokens_kernel<NBITS, F16, MATS, 64, false>;
+    else if (j.group_size == 32)
+      kernel = any ? few_tokens_kernel<NBITS, F16, MATS, 32, true>
+                   : few_tokens_kernel<NBITS, F16, MATS, 32, false>;
+    else if (j.group_size == 16 && !any)
+      kernel = few_tokens_kernel<NBITS, F16, MATS, 16, false>;
+  }
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));

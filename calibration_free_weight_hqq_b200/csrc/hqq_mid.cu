@@ -27,7 +27,7 @@ bool mid_plan(const MidJob& j, MidPlan* plan) {
   p.row_tiles = static_cast<int>(row_tiles);
   // every SM, but at least two k-blocks each: fewer cost more in partial tiles than they save
   p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms, units / 2)));
-  const uint32_t ring = 64u * kMidDqWarps * chunk_bytes(j.nbits) * mid_depth(j.nbits);
+  const uint32_t ring = static_cast<uint32_t>(kMidDqWarps * mid_codes(j.nbits, j.mode) * mid_depth(j.nbits, j.mode));
   const uint32_t stage = 2 * kMidTileBytes + static_cast<uint32_t>(p.tok) * 2 * mid_bk(j.mode);
   p.stages = static_cast<int>(std::min<uint32_t>(4, (232448u - 2048u - ring) / stage));
   p.off_ring = p.stages * stage;

@@ -19,13 +19,17 @@ constexpr int kMidThreads = 32 * (2 + kMidDqWarps + kMidEpiWarps);
 constexpr uint32_t kMidTileBytes = kMidRows * kMidLine * 2;  // a 128 x 64 tile of W'
 constexpr int64_t kMidMaxCols = int64_t(1) << 24;  // 32-bit offsets inside a tile's 128 rows
 
-// Stages of a warp whose codes are in flight: 32 KB of them a CTA, 8 at most.
-__host__ __device__ constexpr int mid_depth(int nbits) {
-  const int n = 32768 / (64 * kMidDqWarps * chunk_bytes(nbits));
+enum MidMode : int { kMidLinear = 0, kMidGated = 1, kMidBackward = 2 };
+
+// Bytes of a warp's codes of a stage, and stages whose codes are in flight: 32 KB of them a CTA, 8 at
+// most.
+__host__ __device__ constexpr int mid_codes(int nbits, int mode) {
+  return mode == kMidGated ? 2 * tile_bytes(nbits, 64) : tile_bytes(nbits, 128);
+}
+__host__ __device__ constexpr int mid_depth(int nbits, int mode) {
+  const int n = 32768 / (kMidDqWarps * mid_codes(nbits, mode));
   return n < 1 ? 1 : n > 8 ? 8 : n;
 }
-
-enum MidMode : int { kMidLinear = 0, kMidGated = 1, kMidBackward = 2 };
 
 // Contraction per k-block, a stage: two W' tiles each, of consecutive lines or, in the gated form, of
 // gate and up. (Stages of one tile left the warp that issues the MMAs as the pace: its wait and

@@ -18,8 +18,8 @@
 //   * Work: all tiles' k-blocks in one line, cut evenly over the CTAs. A CTA that has a tile's whole
 //     contraction writes the result; partial tiles go to the workspace in fp32 and a second kernel
 //     adds them in order (deterministic).
-//   * Codes come by asynchronous copies several tiles ahead, each thread into its own slots; scale and
-//     zero one tile ahead in registers.
+//   * Codes come by asynchronous copies some stages ahead, each warp its own 16 rows; scale and zero
+//     one stage ahead in registers.
 // Every wait is bounded (about two seconds); on expiry the CTA raises an abort flag, counts the
 // timeout, skips its remaining work, waits for its copies in flight and frees its TMEM.
 #pragma once
@@ -98,8 +98,8 @@ __device__ __forceinline__ void mid_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// GROUP: 64 (groups of 64 codes or more), 32, 16 (cols a multiple of 32 with both) or 8 (any group size
-// and cols; codes and meta read where they are used). ANY: see RawMeta.
+// GROUP: 64 (groups of 64 codes or more), 32, 16 (whole_rows) or 8 (any group size and cols; codes and
+// meta read where they are used). ANY: see RawMeta.
 template <int NBITS, bool F16, int MODE, int GROUP, bool ANY>
 __global__ void __launch_bounds__(kMidThreads, 1)
     mid_tokens_kernel(const __grid_constant__ CUtensorMap map_x0,
@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   constexpr int kGroups = GROUP >= 32 ? 1 : 32 / GROUP;
   constexpr bool kShared = MODE != kMidGated && GROUP >= 64;  // both chunks lie in one group
   constexpr int kBK = mid_bk(MODE);
-  constexpr int kDepth = mid_depth(NBITS);
-  constexpr int kSlot = 32 * chunk_bytes(NBITS);  // a warp's chunks of one kind
-  constexpr int kPiece = NBITS == 3 ? 4 : NBITS >= 4 ? 16 : 4 * NBITS;
+  constexpr int kDepth = mid_depth(NBITS, MODE);
+  using Tile = CodeTile<NBITS, kBK, false>;
+  constexpr int kTile = tile_bytes(NBITS, kBK);  // a warp's codes of a stage (of either weight)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -256,9 +256,9 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     const uint32_t gpr = cols >> a.w.lg_group;
     // The thread's row of the block of the weight, and which half of the columns: eight lanes in a row
     // write eight different 16-byte pieces of the swizzled lines (no bank conflicts).
-    const uint32_t r = 16 * wi + (lane & 7) + 8 * (lane >> 4), half = (lane >> 3) & 1;
+    const uint32_t row16 = (lane & 7) + 8 * (lane >> 4), r = 16 * wi + row16, half = (lane >> 3) & 1;
     const uint32_t cc = (MATS == 2 ? 32 : 64) * half;
-    uint8_t* ring = smem + a.p.off_ring + (warp - 2) * (kDepth * 2 * kSlot) + lane * kPiece;
+    uint8_t* ring = smem + a.p.off_ring + (warp - 2) * (kDepth * MATS * kTile);
     const uint32_t ring_u = smem_u32(ring);
     // Where chunk h goes in a stage: line_at + h * line_h, pieces piece0 + h * piece_h ..
     //   linear: the halves are the stage's two tiles, a thread's chunks one line of its tile;
@@ -272,82 +272,77 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     const uint32_t piece0 = MATS == 2 ? 4 * half : 0u;
     constexpr uint32_t piece_h = MATS == 2 ? 0 : 4;
 
-    // Where a walk along the group's stages stands: unit `pos` of the CTA, its tile and k-block, and the
-    // weight, first row and first column of its block.
-    struct Walk {
-      uint32_t pos, tile, kb, mat, row, col;
-    };
-    auto place = [&](Walk& w, bool new_tile) {
-      if (new_tile) {
-        const uint32_t block = w.tile / a.p.tok_tiles * kMidRows;
-        if constexpr (MODE == kMidBackward)
-          w.col = block;
-        else
-          w.row = block;
-      }
-      if constexpr (MODE == kMidBackward) {
-        w.mat = w.kb >= static_cast<uint32_t>(a.p.kb1) ? 1 : 0;
-        w.row = (w.kb - w.mat * a.p.kb1) * kBK;
-      } else {
-        w.col = w.kb * kBK;
-      }
-    };
-    auto start = [&]() {
-      Walk w;
-      w.pos = group;
-      w.tile = (first + group) / KB;
-      w.kb = first + group - w.tile * KB;
-      w.mat = 0;
-      place(w, true);
-      return w;
-    };
-    auto advance = [&](Walk& w) {  // to the group's next stage; whether that is another tile's
-      w.pos += 2;
-      w.kb += 2;
-      const bool other = w.kb >= KB;
-      while (w.kb >= KB) {
-        w.kb -= KB;
-        ++w.tile;
-      }
-      place(w, other);
-      return other;
-    };
     const uint32_t row_codes = r * cols + cc, row_meta = r * gpr;  // the thread's part of an offset
 
-    Walk cw = start(), mw = cw, w = cw;
-    // codes: the block's first byte (3 bits: word) in either weight of a stage
+    // A walk along the group's stages (every second unit of the CTA): where it stands, and how many
+    // more of its stages follow in the same tile and weight. Only a new one costs divisions.
+    struct Walk {
+      uint32_t pos, run, mat, row, col;
+    };
+    auto enter = [&](Walk& w) {
+      const uint32_t tile = (first + w.pos) / KB, kb = first + w.pos - tile * KB;
+      const uint32_t block = tile / a.p.tok_tiles * kMidRows;
+      uint32_t end = KB;
+      w.mat = 0;
+      if constexpr (MODE == kMidBackward) {
+        const uint32_t kb1 = static_cast<uint32_t>(a.p.kb1);
+        w.mat = kb >= kb1 ? 1 : 0;
+        if (kb < kb1) end = kb1;
+        w.row = (kb - w.mat * kb1) * kBK;
+        w.col = block;
+      } else {
+        w.row = block;
+        w.col = kb * kBK;
+      }
+      w.run = (end - kb + 1) / 2;
+    };
+    // One stage on; false where that is another tile or weight, and enter() has run.
+    auto step = [&](Walk& w) {
+      w.pos += 2;
+      if constexpr (MODE == kMidBackward)
+        w.row += 2 * kBK;
+      else
+        w.col += 2 * kBK;
+      if (--w.run != 0) return true;
+      if (w.pos < count) enter(w);
+      return false;
+    };
+
+    // codes: where the warp's 16 rows begin (3 bits: the word) in either weight of a stage
+    Walk cw{};
     const uint8_t* copy_base[MATS];
     uint32_t copy_code0[MATS];
+    const uint32_t row_step = NBITS == 3 ? cols : cols / 8 * NBITS;
     auto aim_copies = [&]() {
-      const int64_t e0 = static_cast<int64_t>(cw.row) * cols;
+      const int64_t e0 = static_cast<int64_t>(cw.row + 16 * wi) * cols;
 #pragma unroll
       for (int i = 0; i < MATS; ++i) {
         copy_base[i] = a.w.packed[MATS == 2 ? i : cw.mat] + (NBITS == 3 ? e0 / 10 * 4 : e0 / 8 * NBITS);
         copy_code0[i] = NBITS == 3 ? static_cast<uint32_t>(e0 % 10) : 0u;
       }
     };
+    const int64_t codes_down = static_cast<int64_t>(2 * kBK) * cols / 8 * NBITS;  // two k-blocks of rows
     auto copy_next = [&](uint32_t slot) {
       if (cw.pos < count) {
-        const uint32_t col = cw.col + cc, e = row_codes + cw.col;
-        if (cw.row + r < rows) {
+        if (cw.row + 16 * wi < rows && cw.col < cols) {
+          const uint32_t have = min(16u, rows - cw.row - 16 * wi);
+          const uint32_t codes = min(static_cast<uint32_t>(kBK), cols - cw.col);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t more = MATS == 2 ? 0 : 32 * h;
-            if (col + more >= cols) break;
-            const uint32_t to = ring_u + (slot * 2 + h) * kSlot;
-            const int i = MATS == 2 ? h : 0;
-            if constexpr (NBITS == 3)
-              copy_chunk<NBITS>(to, copy_base[i], copy_code0[i] + e + more);
-            else
-              copy_chunk<NBITS>(to, copy_base[i], (e + more) / 32 * (4 * NBITS));
-          }
+          for (int i = 0; i < MATS; ++i)
+            Tile::copy(ring_u + (slot * MATS + i) * kTile,
+                       copy_base[i] + (NBITS == 3 ? 0u : cw.col / 8 * NBITS), copy_code0[i] + cw.col,
+                       row_step, have, codes, lane);
         }
-        if (advance(cw) || MODE == kMidBackward) aim_copies();
+        if (!step(cw) || (MODE == kMidBackward && NBITS == 3))
+          aim_copies();
+        else if constexpr (MODE == kMidBackward)
+          copy_base[0] += codes_down;
       }
       cp_async_commit();
     };
-    // scale and zero of the two chunks
+    // scale and zero of the two chunks, a stage ahead
     constexpr int kMeta = kShared ? 1 : 2;
+    Walk mw{};
     Slab slab[MATS];
     RawMeta<ANY> next[kMeta][kGroups];
     auto aim = [&]() {
@@ -355,9 +350,19 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       for (int i = 0; i < MATS; ++i)
         slab[i] = slab_of_row<NBITS, ANY>(a.w, MATS == 2 ? i : mw.mat, mw.row, cols, gpr);
     };
+    const int64_t meta_down = static_cast<int64_t>(2 * kBK) * gpr * 2;
+    auto step_meta = [&]() {
+      const bool same = step(mw);
+      if (MODE == kMidBackward && same && !ANY && kWhole && NBITS != 3) {
+        slab[0].scale += meta_down;
+        slab[0].zero += meta_down;
+      } else if ((!same || MODE == kMidBackward) && mw.pos < count) {
+        aim();
+      }
+    };
     auto fetch_meta = [&]() {
-      const uint32_t col = mw.col + cc;
       if (mw.pos >= count || mw.row + r >= rows) return;
+      const uint32_t col = mw.col + cc;
 #pragma unroll
       for (int h = 0; h < kMeta; ++h) {
 #pragma unroll
@@ -368,9 +373,12 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         }
       }
     };
-    if (w.pos < count) {
+    mw.pos = cw.pos = group;
+    if (group < count) {
+      enter(mw);
       aim();
       if constexpr (kWhole) {
+        cw = mw;
         aim_copies();
         fetch_meta();
 #pragma unroll 1
@@ -378,9 +386,9 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       }
     }
     uint32_t slot = 0, s = group % stages, phase = group >= stages ? 0 : 1;
-    for (; w.pos < count; advance(w)) {
-      const uint32_t col = w.col + cc;
-      const bool in_row = w.row + r < rows;
+    while (mw.pos < count) {
+      const uint32_t at0 = mw.col + cc, codes0 = row_codes + mw.col;
+      const bool in_row = mw.row + r < rows;
       if constexpr (kWhole) {
         GroupMeta m[kMeta][kGroups];
         bool one = !ANY;
@@ -390,22 +398,25 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           for (int u = 0; u < kGroups; ++u) {
             float2 sz = meta_f32_pair<ANY, F16>(next[h][u], slab[MATS == 2 ? h : 0], a.w.meta_dt);
             // W' = 0 outside the weight
-            if (!in_row || col + (MATS == 2 ? 0 : 32 * h) + GROUP * u >= cols) sz = make_float2(0.0f, 0.0f);
+            if (!in_row || at0 + (MATS == 2 ? 0 : 32 * h) + GROUP * u >= cols) sz = make_float2(0.0f, 0.0f);
             m[h][u] = group_meta<NBITS>(sz.x, sz.y, &one);
           }
         one = !ANY && __all_sync(0xFFFFFFFFu, one);
-        uint32_t off[MATS];
+        uint32_t first_slot[MATS];  // 3 bits: the row's first code's place in its word
 #pragma unroll
-        for (int i = 0; i < MATS; ++i) off[i] = slab[i].code0 + row_codes + w.col;
-        if ((advance(mw) || MODE == kMidBackward) && mw.pos < count) aim();
+        for (int i = 0; i < MATS; ++i)
+          first_slot[i] = NBITS == 3 ? (slab[i].code0 + codes0 - cc) % 10u : 0u;
+        step_meta();
         fetch_meta();
-        cp_async_wait<kDepth - 1>();  // the thread's own copies: no other reads them
+        cp_async_wait<kDepth - 1>();
+        __syncwarp();  // every lane's copies have landed
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(kMidEmpty + s), phase, abort_flag))) break;
         uint8_t* to = smem + s * stage_bytes + line_at;
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
-          const Codes32<NBITS> c = read_chunk<NBITS>(ring + (slot * 2 + h) * kSlot,
-                                                     MATS == 2 ? off[h] : off[0] + 32 * h);
+          const int i = MATS == 2 ? h : 0;
+          const Codes32<NBITS> c = Tile::read(ring + (slot * MATS + i) * kTile, row16,
+                                              cc + (MATS == 2 ? 0 : 32 * h), first_slot[i]);
           uint4 o[4];
           if (one)
             dequant_chunk<NBITS, OUT, kGroups, true>(c, m[kShared ? 0 : h], o);
@@ -416,19 +427,15 @@ __global__ void __launch_bounds__(kMidThreads, 1)
             *reinterpret_cast<uint4*>(to + h * line_h + (((piece0 + h * piece_h + u) ^ (r & 7)) << 4)) = o[u];
         }
       } else {
-        if (w.pos != mw.pos) {
-          mw = w;
-          aim();
-        }
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar(kMidEmpty + s), phase, abort_flag))) break;
         uint8_t* to = smem + s * stage_bytes + line_at;
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
           const Slab& b = slab[MATS == 2 ? h : 0];
-          const uint32_t more = MATS == 2 ? 0 : 32 * h, at = col + more;
+          const uint32_t more = MATS == 2 ? 0 : 32 * h, at = at0 + more;
           const uint32_t left = in_row && at < cols ? min(4u, (cols - at) / 8) : 0u;
-          const Codes32<NBITS> c = load_codes_units<NBITS>(b.codes, b.code0 + row_codes + w.col + more,
-                                                           static_cast<int>(left));
+          const Codes32<NBITS> c =
+              load_codes_units<NBITS>(b.codes, b.code0 + codes0 + more, static_cast<int>(left));
           GroupMeta m[4];
           bool one = false;
 #pragma unroll
@@ -446,12 +453,13 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           for (uint32_t u = 0; u < 4; ++u)
             *reinterpret_cast<uint4*>(to + h * line_h + (((piece0 + h * piece_h + u) ^ (r & 7)) << 4)) = o[u];
         }
+        step_meta();
       }
       fence_proxy_async_smem();  // generic-proxy writes -> read by the tensor core
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kMidFull + s));
       s += 2;  // the other group fills the stage between
-      while (s >= stages) {
+      if (s >= stages) {
         s -= stages;
         phase ^= 1;
       }
@@ -582,16 +590,18 @@ cudaError_t launch_mid_mode(const MidJob& j, const MidPlan& plan, cudaStream_t s
   a.out = MODE == kMidBackward ? a.cols : a.rows;
   a.act = j.act;
   a.p = plan;
-  const bool any = any_meta(j.w, j.weights, j.meta_dtype, j.x_dtype), whole = j.cols % 32 == 0;
+  const bool any = any_meta(j.w, j.weights, j.meta_dtype, j.x_dtype);
   auto kernel = mid_tokens_kernel<NBITS, F16, MODE, 8, true>;
-  if (j.group_size >= 64)
-    kernel = any ? mid_tokens_kernel<NBITS, F16, MODE, 64, true>
-                 : mid_tokens_kernel<NBITS, F16, MODE, 64, false>;
-  else if (j.group_size == 32)
-    kernel = any ? mid_tokens_kernel<NBITS, F16, MODE, 32, true>
-                 : mid_tokens_kernel<NBITS, F16, MODE, 32, false>;
-  else if (whole && j.group_size == 16 && !any)
-    kernel = mid_tokens_kernel<NBITS, F16, MODE, 16, false>;
+  if (whole_rows(NBITS, j.cols)) {
+    if (j.group_size >= 64)
+      kernel = any ? mid_tokens_kernel<NBITS, F16, MODE, 64, true>
+                   : mid_tokens_kernel<NBITS, F16, MODE, 64, false>;
+    else if (j.group_size == 32)
+      kernel = any ? mid_tokens_kernel<NBITS, F16, MODE, 32, true>
+                   : mid_tokens_kernel<NBITS, F16, MODE, 32, false>;
+    else if (j.group_size == 16 && !any)
+      kernel = mid_tokens_kernel<NBITS, F16, MODE, 16, false>;
+  }
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(plan.smem));
   if (e != cudaSuccess) return e;

@@ -5,7 +5,14 @@ namespace hqqk {
 
 constexpr int kSms = 148;  // of a B200
 
-// Bytes that a lane's chunk of 32 codes takes in shared memory (3 bits: the five words it may span).
-__host__ __device__ constexpr int chunk_bytes(int nbits) { return nbits == 3 ? 20 : 4 * nbits; }
+// Bytes of a row of `codes` codes (64, 128 or 256) of a tile in shared memory. At 3 bits: the words it
+// may span, one more where they would be even (rows then start on different banks).
+__host__ __device__ constexpr int tile_row_bytes(int nbits, int codes) {
+  return nbits == 3 ? 4 * (((9 + codes - 1) / 10 + 1) | 1) : codes * nbits / 8;
+}
+// Bytes of a tile of 16 rows.
+__host__ __device__ constexpr int tile_bytes(int nbits, int codes) {
+  return 16 * tile_row_bytes(nbits, codes);
+}
 
 }  // namespace hqqk
