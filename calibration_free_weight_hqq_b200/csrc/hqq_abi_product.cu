@@ -108,9 +108,6 @@ bool use_few(int64_t M, const hqq_weight& w, const hqq_weight* up) {
          hqqk::few_serves(few_job(M, w, up));
 }
 
-// Tokens up to which the some-token kernel serves a product it can take.
-constexpr int64_t kMidMaxTokens = 1024;
-
 hqqk::MidJob mid_job(int mode, int64_t M, const hqq_weight& w, const hqq_weight* up) {
   hqqk::MidJob j = {};
   j.mode = mode;
@@ -127,13 +124,33 @@ hqqk::MidJob mid_job(int mode, int64_t M, const hqq_weight& w, const hqq_weight*
   return j;
 }
 
-// Whether a product runs straight from the codes on the some-token kernel, and what workspace
-// that takes.
+// Whether a product runs straight from the codes on the some-token kernel rather than on dequantized
+// weights, and what workspace that takes. Both times in us are estimated from the sizes:
+//   * from the codes, every token tile converts the weights again: 0.45 ns per thousand codes, and
+//     0.0022 more for each token of the tile;
+//   * dequantized, 0.6 ns per thousand codes to write and read W', then waves of 256 x 256 tiles
+//     over 74 CTA pairs at 0.27 us per 64 of the contraction, and 10 us of launches.
+// Measured in us, 4 bits, 11008 x 4096 (forward) and 4096 x 11008 (gradient), codes / dequantized:
+//   tokens    64        256       512       768       1024
+//   linear    27 / 54   46 / 55   83 / 77  106 / 77  136 / 98
+//   gradient  28 / 52   48 / 53   85 / 73  109 / 74  140 / 94
+//   gated     48 / 113  81 / 114 169 / 133 217 / 154 309 / 175
+//   its grad. 50 / 162  72 / 166 113 / 171 158 / 175 215 / 183
 bool use_mid(int mode, int64_t M, const hqq_weight& w, const hqq_weight* up, size_t* need) {
-  if (M > kMidMaxTokens || w.params.axis != 1) return false;
+  if (w.params.axis != 1) return false;
   if (up != nullptr && !same_format(w.params, up->params)) return false;
   hqqk::MidPlan plan;
   if (!hqqk::mid_plan(mid_job(mode, M, w, up), &plan)) return false;
+  const bool back = mode == hqqk::kMidBackward;
+  const double codes = 1e-6 * static_cast<double>(w.rows) * static_cast<double>(w.cols) * (up ? 2 : 1);
+  const double direct = codes * plan.tok_tiles * (0.45 + 0.0022 * plan.tok);
+  const int64_t out = back ? w.cols : w.rows, inner = back ? w.rows : w.cols;
+  const int64_t tile_n = mode == hqqk::kMidGated ? 128 : 256;
+  const int64_t tiles = ((M + 255) / 256) * ((out + tile_n - 1) / tile_n);
+  const double dense = 0.6 * codes + 10.0 +
+                       0.27 * static_cast<double>((tiles + 73) / 74) *
+                           static_cast<double>((inner + 63) / 64) * (back && up ? 2 : 1);
+  if (direct > dense) return false;
   *need = (plan.partial_bytes + 255) / 256 * 256;
   return true;
 }

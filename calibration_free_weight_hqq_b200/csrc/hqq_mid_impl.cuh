@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
     uint32_t tile = first / KB, kb = first - tile * KB, pos = 0, s = 0, phase = 1;
     int m0 = static_cast<int>((tile % a.p.tok_tiles) * T);
     for (; pos < count; ++pos) {
-      if (!mbar_wait(bar(kMidEmpty + s), phase, abort_flag)) break;
+      if (!mbar_wait_idle(bar(kMidEmpty + s), phase, abort_flag)) break;
       if (lane == 0) {
         const bool second = MODE == kMidBackward && kb >= static_cast<uint32_t>(a.p.kb1);
         const CUtensorMap* map = second ? &map_x1 : &map_x0;
@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       const uint32_t n_kb = min(KB - kb, left), buf = seg % bufs;
       const bool whole = n_kb == KB;
       const bool ok = __all_sync(
-          0xFFFFFFFFu, mbar_wait(bar(kMidAccFull + buf), (seg / bufs) & 1, abort_flag) && !*abort_flag);
+          0xFFFFFFFFu,
+          mbar_wait_idle(bar(kMidAccFull + buf), (seg / bufs) & 1, abort_flag) && !*abort_flag);
       if (!ok) break;
       tc_fence_after();
       const uint32_t row = quarter * 32 + lane;
@@ -522,10 +523,11 @@ __global__ void __launch_bounds__(kMidThreads, 1)
 }
 
 // Tiles that several CTAs share: their partial tiles added in the order of k, then the epilogue.
-// A block takes 32 tokens of a tile, a lane 4 outputs of a token at a time. Launched while the
-// product runs (programmatic dependent launch): it waits for its end first.
+// A block takes 8 tokens of a tile, a warp one of them, a lane 4 outputs. Launched while the
+// product runs (programmatic dependent launch; 32 registers, so that blocks fit beside it): it finds
+// its place first and then waits for the product's end.
 template <bool F16, int MATS>
-__global__ void __launch_bounds__(256) mid_finish_kernel(const MidArgs a) {
+__global__ void __launch_bounds__(256, 8) mid_finish_kernel(const MidArgs a) {
   const uint32_t T = static_cast<uint32_t>(a.p.tok), KB = static_cast<uint32_t>(a.p.kb);
   const uint32_t ctas = static_cast<uint32_t>(a.p.ctas);
   const uint32_t units = static_cast<uint32_t>(a.p.row_tiles * a.p.tok_tiles) * KB;
@@ -534,34 +536,32 @@ __global__ void __launch_bounds__(256) mid_finish_kernel(const MidArgs a) {
   const uint32_t c1 = mid_cta_of(tile * KB + KB - 1, ctas, units);
   // c0 may have begun with an earlier tile (then this one is its last); the others begin with this
   const uint32_t slot0 = 2 * c0 + (mid_first_unit(c0, ctas, units) / KB != tile ? 1 : 0);
-  const uint32_t row = (threadIdx.x & 31) * 4;
+  const uint32_t row = (threadIdx.x & 31) * 4, t = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int n = static_cast<int>(tile / a.p.tok_tiles * kMidRows + row);
-  const int64_t tok0 = static_cast<int64_t>(tile % a.p.tok_tiles) * T;
+  const int64_t tok = static_cast<int64_t>(tile % a.p.tok_tiles) * T + t;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c0 == c1 || n >= a.out) return;
+  if (c0 == c1 || n >= a.out || t >= T || tok >= a.M) return;
   const size_t slot = static_cast<size_t>(MATS) * T * kMidRows;
-  const uint32_t end = min(T, (blockIdx.y + 1) * 32);
-  for (uint32_t t = blockIdx.y * 32 + (threadIdx.x >> 5); t < end; t += 8) {
-    if (tok0 + t >= a.M) return;
-    float s[MATS][4];
+  float4 s[MATS];
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+    s[m] = __ldcg(reinterpret_cast<const float4*>(
+        a.partial + slot0 * slot + (static_cast<size_t>(m) * T + t) * kMidRows + row));
+#pragma unroll 2
+  for (uint32_t c = c0 + 1; c <= c1; ++c) {
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
-      const float* part = a.partial + (static_cast<size_t>(m) * T + t) * kMidRows + row;
-      float4 v = __ldcg(reinterpret_cast<const float4*>(part + slot0 * slot));
-      for (uint32_t c = c0 + 1; c <= c1; ++c) {
-        const float4 p = __ldcg(reinterpret_cast<const float4*>(part + 2 * c * slot));
-        v = make_float4(__fadd_rn(v.x, p.x), __fadd_rn(v.y, p.y), __fadd_rn(v.z, p.z),
-                        __fadd_rn(v.w, p.w));
-      }
-      s[m][0] = v.x;
-      s[m][1] = v.y;
-      s[m][2] = v.z;
-      s[m][3] = v.w;
+      const float4 p = __ldcg(reinterpret_cast<const float4*>(
+          a.partial + 2 * c * slot + (static_cast<size_t>(m) * T + t) * kMidRows + row));
+      s[m] = make_float4(__fadd_rn(s[m].x, p.x), __fadd_rn(s[m].y, p.y), __fadd_rn(s[m].z, p.z),
+                         __fadd_rn(s[m].w, p.w));
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      mid_store<F16, MATS>(a, tok0 + t, n + q, s[0][q], MATS == 2 ? s[MATS - 1][q] : 0.0f);
   }
+  const float4 g = s[0], u = s[MATS - 1];
+  mid_store<F16, MATS>(a, tok, n, g.x, u.x);
+  mid_store<F16, MATS>(a, tok, n + 1, g.y, u.y);
+  mid_store<F16, MATS>(a, tok, n + 2, g.z, u.z);
+  mid_store<F16, MATS>(a, tok, n + 3, g.w, u.w);
 }
 
 // ---------------------------------------------------------------- host side
@@ -616,7 +616,7 @@ cudaError_t launch_mid_mode(const MidJob& j, const MidPlan& plan, cudaStream_t s
   cfg.numAttrs = 1;
   cfg.stream = st;
   cfg.gridDim = dim3(static_cast<unsigned>(plan.row_tiles * plan.tok_tiles),
-                     static_cast<unsigned>((plan.tok + 31) / 32));
+                     static_cast<unsigned>((plan.tok + 7) / 8));
   cfg.blockDim = dim3(256);
   return cudaLaunchKernelEx(&cfg, mid_finish_kernel<F16, MODE == kMidGated ? 2 : 1>, a);
 }

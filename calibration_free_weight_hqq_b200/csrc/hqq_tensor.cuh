@@ -63,6 +63,23 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     }
   }
 }
+// The same for a warp that others need the issue slots of more than it needs the first nanoseconds:
+// it sleeps between its looks.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity,
+                                               volatile uint32_t* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    __nanosleep(100);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicAdd(&g_wait_timeouts, 1u);
+      return false;
+    }
+  }
+}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             uint32_t bar) {
   asm volatile(
