@@ -246,3 +246,364 @@ def test_gated_backward(M, N, K, dtype, act):
     close(host(dX), rG @ gate.W + rU @ up.W, 2 * N * 2.0 ** -23 * S, dtype, "dX")
     close(host(dbg), rG.sum(0), M * 2.0 ** -23 * np.abs(rG).sum(0), dtype, "dbias_gate")
     close(host(dbu), rU.sum(0), M * 2.0 ** -23 * np.abs(rU).sum(0), dtype, "dbias_up")
+
+
+# ------------------------------------------------------------------ dequantized weights (axis 0)
+
+@pytest.mark.parametrize("M,N,K", [(9, 64, 72), (33, 264, 256), (128, 256, 64), (257, 776, 328),
+                                   (600, 1032, 520), (2500, 264, 136)])
+@pytest.mark.parametrize("dtype,act,bias", [("bf16", "silu", True), ("f16", "gelu", False),
+                                            ("bf16", "gelu_tanh", False)])
+def test_groups_down_the_columns(M, N, K, dtype, act, bias):
+    gate = Layer(N, K, 4, 8, 0, dtype, bias=bias, seed=M + N)
+    up = Layer(N, K, 4, 8, 0, dtype, bias=bias, seed=M + N + 1)
+    X, X64 = draw((M, K), M, dtype, scale=0.5 / np.sqrt(K) / np.abs(gate.W).max())
+    S, e = up.project(X64)
+    close(host(hqq.hqq_linear_ex(X, up.h)), S, e, dtype, "Y")
+    check_gated(M, N, K, act, dtype, gate, up, X, X64)
+
+
+@pytest.mark.parametrize("M,N,K", [(2304, 2048, 2048), (4100, 1032, 4096)])
+def test_many_tokens_along_the_rows(M, N, K):
+    """Enough work that the weight is dequantized once; checked on sampled tokens."""
+    gate, up = (Layer(N, K, 4, 64, 1, "bf16", seed=s) for s in (1, 2))
+    X, X64 = draw((M, K), 3, "bf16", scale=0.02)
+    rows = np.r_[0:3, M // 2:M // 2 + 3, M - 3:M]
+    Y, G, U = hqq.hqq_gated_linear(X, gate.h, up.h, save=True)
+    g, eg = gate.project(X64[rows])
+    u, eu = up.project(X64[rows])
+    a, _ = act64("silu", g)
+    assert np.abs(g).max() < 20
+    close(host(G)[rows], g, eg, "bf16", "G")
+    close(host(U)[rows], u, eu, "bf16", "U")
+    ea = 1.2 * eg + ACT_REL["silu"] * np.abs(a) + 1e-12
+    close(host(Y)[rows], a * u, ea * np.abs(u) + (np.abs(a) + ea) * eu + 2.0 ** -23 * np.abs(a * u),
+          "bf16", "Y")
+    S, e = up.project(X64[rows])
+    close(host(hqq.hqq_linear_ex(X, up.h))[rows], S, e, "bf16", "Y of one weight")
+    dY, dY64 = draw((M, N), 4, "bf16")
+    dX = host(hqq.hqq_linear_backward(dY, gate.h))[rows]
+    close(dX, dY64[rows] @ gate.W, N * 2.0 ** -23 * (np.abs(dY64[rows]) @ np.abs(gate.W)), "bf16", "dX")
+
+
+# ------------------------------------------------------------------ odd scales and zeros
+
+@pytest.mark.parametrize("nbits", NBITS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("meta", ["same", "f32"])
+def test_one_hot_with_odd_scales_and_zeros(nbits, dtype, meta):
+    """Zeros next to 0, negative, far outside the codes and far beyond them; scale 0 and tiny."""
+    N, K, G = 32, 320, 64
+    rng = np.random.default_rng(nbits)
+    codes = rng.integers(0, 2 ** nbits, size=N * K, dtype=np.uint8)
+    ng = N * K // G
+    zero = rng.choice([0.0, -0.0, 1e-3, -1e-3, 0.37, 7.5, -5.0, 123.0, -1000.0, 4097.0, 3e4, 1e-7], ng)
+    scale = rng.choice([0.0, 1e-4, 0.01, 1.0, -0.5, 3e-6], ng)
+    kind = dtype if meta == "same" else "f32"
+    zero = oracle.round_to_dtype(zero.astype(np.float32), kind)
+    scale = oracle.round_to_dtype(scale.astype(np.float32), kind)
+    W = oracle.round_to_dtype(oracle.dequantize(codes, scale, zero, N, K, G, 1), dtype)
+    prm = hqq.make_params(nbits, G, 1, w_dtype=TORCH[dtype], meta_dtype=TORCH[kind])
+    q = [torch.from_numpy(oracle.pack(codes, nbits)).cuda()] + \
+        [torch.from_numpy(v).to(TORCH[kind]).cuda() for v in (scale, zero)]
+    w = hqq.quantized_weight(q, N, K, prm)
+    eye = torch.eye(K, dtype=TORCH[dtype], device="cuda")
+    for n in (8, 40):
+        for k0 in range(0, K, n):
+            got = host(hqq.hqq_linear_ex(eye[k0:k0 + n], w))
+            assert np.array_equal(got, W.T[k0:k0 + n].astype(np.float64))
+    got = host(hqq.hqq_linear_backward(torch.eye(N, dtype=TORCH[dtype], device="cuda"), w))
+    assert np.array_equal(got, W.astype(np.float64))
+
+
+@pytest.mark.parametrize("run", [8, 24, 100, 1024])
+def test_second_level_runs(run):
+    for M in (3, 50):
+        L = Layer(136, 448, 4, 64, 1, "bf16", "u8", seed=run, run=run)
+        X, X64 = draw((M, 448), run, "bf16")
+        S, e = L.project(X64)
+        close(host(hqq.hqq_linear_ex(X, L.h)), S, e, "bf16", "Y")
+        dY, dY64 = draw((M, 136), run, "bf16")
+        e = 136 * 2.0 ** -23 * (np.abs(dY64) @ np.abs(L.W))
+        close(host(hqq.hqq_linear_backward(dY, L.h)), dY64 @ L.W, e, "bf16", "dX")
+
+
+def test_meta_and_bias_views_of_natural_alignment():
+    """Scale, zero and bias that start on an odd element."""
+    N, K = 72, 320
+    L = Layer(N, K, 4, 64, 1, "bf16", bias=True, seed=9)
+
+    def shifted(t):
+        big = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        big[1:] = t.reshape(-1)
+        return big[1:]
+
+    pk, sc, zr = L.h.tensors[:3]
+    w = hqq.quantized_weight((pk, shifted(sc), shifted(zr)), N, K, L.params,
+                             bias=shifted(L.h.tensors[-1]))
+    for M in (1, 40):
+        X, _ = draw((M, K), M, "bf16")
+        assert torch.equal(hqq.hqq_linear_ex(X, w), hqq.hqq_linear_ex(X, L.h))
+
+
+# ------------------------------------------------------------------ infinities, empty, untouched rows
+
+@pytest.mark.parametrize("M", [5, 40, 300])
+@pytest.mark.parametrize("axis", [1, 0])
+def test_a_token_of_infinities_stays_alone(M, axis):
+    L = Layer(264, 320, 4, 8, axis, "bf16", seed=2)
+    X, _ = draw((M, 320), 1, "bf16")
+    clean = hqq.hqq_linear_ex(X, L.h)
+    X[2, 7], X[3, 0] = float("inf"), float("nan")
+    got = hqq.hqq_linear_ex(X, L.h)
+    keep = [m for m in range(M) if m not in (2, 3)]
+    assert torch.equal(got[keep], clean[keep])
+    assert torch.isnan(got[3]).all() and not torch.isfinite(got[2]).any()
+    dY, _ = draw((M, 264), 1, "bf16")
+    clean = hqq.hqq_linear_backward(dY, L.h)
+    dY[2, 7] = float("inf")
+    got = hqq.hqq_linear_backward(dY, L.h)
+    keep = [m for m in range(M) if m != 2]
+    assert torch.equal(got[keep], clean[keep]) and not torch.isfinite(got[2]).any()
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_a_feature_of_infinite_scale_stays_alone(M):
+    N, K = 40, 256
+    L = Layer(N, K, 4, 64, 1, "bf16", seed=2)
+    X, _ = draw((M, K), 1, "bf16")
+    clean = hqq.hqq_linear_ex(X, L.h)
+    L.h.tensors[1].view(N, -1)[5, 1] = float("inf")
+    got = hqq.hqq_linear_ex(X, L.h)
+    keep = [n for n in range(N) if n != 5]
+    assert torch.equal(got[:, keep], clean[:, keep]) and not torch.isfinite(got[:, 5]).any()
+
+
+@pytest.mark.parametrize("M", [0, 1, 8, 9, 100, 300])
+def test_rows_behind_the_last_token_stay_as_they_were(M):
+    N, K = 136, 192
+    gate, up = (Layer(N, K, 4, 64, 1, "bf16", seed=s) for s in (1, 2))
+    X, _ = draw((max(M, 1), K), 1, "bf16")
+    X = X[:M]
+    bufs = [torch.full((M + 3, N), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(5)]
+    Y, G, U, dG, dU = (b[:M] for b in bufs)
+    last = torch.full((M + 3, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    hqq.hqq_gated_linear(X, gate.h, up.h, Y=Y, G=G, U=U)
+    hqq.hqq_gated_linear_backward(Y, G, U, gate.h, up.h, dX=last[:M], dG=dG, dU=dU)
+    torch.cuda.synchronize()
+    for b in (*bufs, last):
+        assert (b[M:] == 7.0).all()
+        assert not (b[:M] == 7.0).all() or M == 0
+
+
+@pytest.mark.parametrize("axis", [1, 0])
+def test_empty_shapes(axis):
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    L = Layer(64, 64, 4, 64, axis, "bf16", bias=True, seed=1)
+    assert hqq.hqq_linear_ex(torch.empty(0, 64, **bf), L.h).shape == (0, 64)
+    dX, db = hqq.hqq_linear_backward(torch.empty(0, 64, **bf), L.h, bias_grad=True)
+    assert dX.shape == (0, 64) and (db == 0).all()
+    out = hqq.hqq_gated_linear_backward(*[torch.empty(0, 64, **bf)] * 3, L.h, L.h, bias_grad=True)
+    assert [tuple(t.shape) for t in out] == [(0, 64)] * 3 + [(64,)] * 2
+    assert (out[3] == 0).all() and (out[4] == 0).all()
+    # no input features: every sum is the bias
+    none = torch.empty(0, **bf)
+    prm = hqq.make_params(4, 64, axis, w_dtype=torch.bfloat16)
+    b = torch.randn(64, device="cuda").bfloat16()
+    w = hqq.quantized_weight((torch.empty(0, dtype=torch.uint8, device="cuda"), none, none), 64, 0,
+                             prm, bias=b)
+    for M in (1, 70000):
+        X = torch.empty(M, 0, **bf)
+        assert torch.equal(hqq.hqq_linear_ex(X, w), b.expand(M, 64))
+        Y, G, U = hqq.hqq_gated_linear(X, w, w, save=True)
+        assert torch.equal(G, b.expand(M, 64)) and torch.equal(U, G)
+    dY = torch.randn(5, 64, device="cuda").bfloat16()
+    dX, db = hqq.hqq_linear_backward(dY, w, bias_grad=True)
+    assert dX.shape == (5, 0)
+    close(host(db), host(dY).sum(0), 5 * 2.0 ** -23 * np.abs(host(dY)).sum(0), "bf16", "dbias")
+    # no output features: nothing forward, an empty sum back
+    w = hqq.quantized_weight((torch.empty(0, dtype=torch.uint8, device="cuda"), none, none), 0, 64, prm)
+    assert hqq.hqq_linear_ex(torch.empty(3, 64, **bf), w).shape == (3, 0)
+    assert (hqq.hqq_linear_backward(torch.empty(3, 0, **bf), w) == 0).all()
+    assert (hqq.hqq_gated_linear_backward(*[torch.empty(3, 0, **bf)] * 3, w, w)[0] == 0).all()
+
+
+# ------------------------------------------------------------------ streams, graphs, repetition
+
+def block(seed=0, N=328, K=192, dtype="bf16"):
+    gate, up = (Layer(N, K, 4, 64, 1, dtype, seed=seed + s) for s in (1, 2))
+    down = Layer(K, N, 2, 8, 1, dtype, seed=seed + 3)
+    return gate, up, down
+
+
+def run_block(X, dOut, gate, up, down):
+    """Forward and backward of a feed-forward block: every operator as they are used together."""
+    Y, G, U = hqq.hqq_gated_linear(X, gate.h, up.h, save=True)
+    out = hqq.hqq_linear_ex(Y, down.h)
+    dY = hqq.hqq_linear_backward(dOut, down.h)
+    dX, dG, dU = hqq.hqq_gated_linear_backward(dY, G, U, gate.h, up.h)
+    return out, Y, G, U, dY, dX, dG, dU
+
+
+@pytest.mark.parametrize("M", [1, 7, 70, 700])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_feed_forward_block(M, dtype):
+    """The chain, each step held to the formula on the inputs it was given, and the whole gradient
+    to that of the block in 64 bits."""
+    gate, up, down = block(dtype=dtype)
+    X, X64 = draw((M, 192), 5, dtype, scale=0.05)
+    dOut, dOut64 = draw((M, 192), 6, dtype, scale=0.1)
+    out, Y, G, U, dY, dX, dG, dU = run_block(X, dOut, gate, up, down)
+    S, e = down.project(host(Y))
+    close(host(out), S, e, dtype, "out")
+    e = 192 * 2.0 ** -23 * (np.abs(dOut64) @ np.abs(down.W))
+    close(host(dY), dOut64 @ down.W, e, dtype, "dY")
+    a, d = act64("silu", host(G))
+    close(host(dU), host(dY) * a, np.abs(host(dY)) * (2 * ACT_REL["silu"] * np.abs(a) + 1e-12), dtype, "dU")
+    # against the gradient of the 64-bit block: each rounded tensor on the way adds half a step to
+    # each term of the sums behind it: G, U (act' <= 1.1, |act''| <= 0.5), dY, dG and dU
+    g, u = X64 @ gate.W.T, X64 @ up.W.T
+    a, d = act64("silu", g)
+    dy = dOut64 @ down.W
+    want = (dy * u * d) @ gate.W + (dy * a) @ up.W
+    eps = UNIT[dtype]
+    tg = np.abs(dy * u * d) * 3 * eps + np.abs(dy * u) * 0.5 * eps * np.abs(g)
+    tu = np.abs(dy * a) * 2 * eps + np.abs(dy) * 1.1 * eps * np.abs(g)
+    err = 1.05 * (tg @ np.abs(gate.W) + tu @ np.abs(up.W)) + \
+        2 * 328 * 2.0 ** -23 * (np.abs(dy * u * d) @ np.abs(gate.W) + np.abs(dy * a) @ np.abs(up.W)) + \
+        328 * TINY[dtype] * (np.abs(gate.W).max() + np.abs(up.W).max())
+    close(host(dX), want, err, dtype, "dX of the block")
+
+
+def test_gradient_against_differences():
+    """dX of the block times a direction against central differences of the 64-bit block."""
+    gate, up, down = block()
+    X, X64 = draw((6, 192), 5, "bf16", scale=0.05)
+    dOut, dOut64 = draw((6, 192), 6, "bf16", scale=0.1)
+    dX = host(run_block(X, dOut, gate, up, down)[5])
+
+    def loss(x):
+        a, _ = act64("silu", x @ gate.W.T)
+        return ((a * (x @ up.W.T)) @ down.W.T * dOut64).sum()
+
+    rng = np.random.default_rng(0)
+    for _ in range(4):
+        v = rng.standard_normal(X64.shape)
+        h = 1e-5
+        want = (loss(X64 + h * v) - loss(X64 - h * v)) / (2 * h)
+        # each element of dX is off by some four half steps of bf16 of its own size or of its row's
+        # terms; in a random direction they add like a random walk: six of its standard deviations
+        tol = 6 * 8 * UNIT["bf16"] * np.sqrt(((np.abs(dX) + np.abs(dX).mean()) ** 2 * v * v).sum())
+        assert abs((dX * v).sum() - want) <= tol
+
+
+@pytest.mark.parametrize("M", [4, 70, 300])
+def test_other_streams(M):
+    """A call on a side stream, with tensors of its own and given ones, gives the same bits."""
+    gate, up, down = block()
+    X, _ = draw((M, 192), 5, "bf16", scale=0.05)
+    dOut, _ = draw((M, 192), 6, "bf16")
+    want = run_block(X, dOut, gate, up, down)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    Y, G, U = hqq.hqq_gated_linear(X, gate.h, up.h, save=True, stream=side)
+    out = hqq.hqq_linear_ex(Y, down.h, stream=side)
+    dY = hqq.hqq_linear_backward(dOut, down.h, stream=side)
+    dX, dG, dU = hqq.hqq_gated_linear_backward(dY, G, U, gate.h, up.h, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(want, (out, Y, G, U, dY, dX, dG, dU)):
+        assert torch.equal(a, b)
+    with torch.cuda.stream(side):
+        for a, b in zip(want, run_block(X, dOut, gate, up, down)):
+            assert torch.equal(a, b)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M", [4, 70, 300])
+def test_graph_replay_follows_its_inputs(M):
+    gate, up, down = block()
+    X, _ = draw((M, 192), 5, "bf16", scale=0.05)
+    dOut, _ = draw((M, 192), 6, "bf16")
+    run_block(X, dOut, gate, up, down)
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run_block(X, dOut, gate, up, down))
+        graphs.append(g)
+    for seed in (7, 8):
+        X.copy_(draw((M, 192), seed, "bf16", scale=0.05)[0])
+        want = run_block(X, dOut, gate, up, down)
+        for o in outs:
+            for t in o:
+                t.zero_()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            for a, b in zip(want, o):
+                assert torch.equal(a, b)
+    del graphs
+
+
+def test_same_bits_every_time_and_with_a_given_workspace():
+    for M, N, K in ((5, 1032, 4096), (100, 392, 4096), (300, 264, 2048)):
+        L = Layer(N, K, 4, 64, 1, "bf16", seed=M)
+        X, _ = draw((M, K), M, "bf16")
+        first = hqq.hqq_linear_ex(X, L.h)
+        ws = torch.full((hqq.hqq_linear_workspace_bytes(M, L.h),), 255, dtype=torch.uint8, device="cuda")
+        for _ in range(3):
+            assert torch.equal(hqq.hqq_linear_ex(X, L.h), first)
+            assert torch.equal(hqq.hqq_linear_ex(X, L.h, workspace=ws), first)
+        X3 = X[:, None, :].contiguous()
+        assert torch.equal(hqq.hqq_linear_ex(X3, L.h)[:, 0], first)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, one weight."""
+    L = Layer(520, 1024, 4, 64, 1, "bf16", seed=3)
+    Xs = [draw((M, 1024), M, "bf16")[0] for M in (60, 90)]
+    want = [hqq.hqq_linear_ex(X, L.h) for X in Xs]
+    streams = [torch.cuda.Stream() for _ in Xs]
+    torch.cuda.synchronize()
+    outs = [[] for _ in Xs]
+    for _ in range(20):
+        for i, (X, s) in enumerate(zip(Xs, streams)):
+            outs[i].append(hqq.hqq_linear_ex(X, L.h, stream=s))
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, y) for y in o)
+
+
+# ------------------------------------------------------------------ a weight beyond 2^32 codes
+
+@pytest.mark.slow
+@pytest.mark.parametrize("N,K", [(69632, 65600), (1100032, 4160)])
+def test_more_than_2_pow_32_codes(N, K):
+    """4 bits, group 64, 4.6e9 codes: code offsets pass 32 bits; checked on rows at the start, around
+    code 2^32 and at the end. One token of the longer rows does not fit the few-token kernel, one
+    of the shorter ones does."""
+    G = 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    packed = torch.randint(0, 256, (N * K // 2,), dtype=torch.uint8, generator=g, device="cuda")
+    scale = (torch.rand(N * K // G, generator=g, device="cuda") * 0.01 + 1e-3).bfloat16()
+    zero = (torch.rand(N * K // G, generator=g, device="cuda") * 15).bfloat16()
+    prm = hqq.make_params(4, G, 1, w_dtype=torch.bfloat16)
+    w = hqq.quantized_weight((packed, scale, zero), N, K, prm)
+    cross = 2 ** 32 // K
+    rows = torch.tensor([0, 1, cross - 1, cross, cross + 1, 2 * cross // 2 + 7, N - 9, N - 1], device="cuda")
+    b = packed.view(N, K // 2)[rows]
+    q = torch.stack([b & 15, b >> 4], -1).view(len(rows), K // G, G).float()
+    s, z = scale.view(N, K // G)[rows].float(), zero.view(N, K // G)[rows].float()
+    W = ((q - z[..., None]) * s[..., None]).bfloat16().double().view(len(rows), K)
+    for M in (1, 9):
+        X = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+        Y = hqq.hqq_linear_ex(X, w)[:, rows]
+        want = X.double() @ W.T
+        e = K * 2.0 ** -23 * (X.double().abs() @ W.abs().T)
+        close(host(Y), want.cpu().numpy(), e.cpu().numpy(), "bf16", "Y")
+    # the gradient of a row of dY that selects weight rows: their W', exactly
+    dY = torch.zeros(len(rows), N, dtype=torch.bfloat16, device="cuda")
+    dY[torch.arange(len(rows), device="cuda"), rows] = 1.0
+    assert torch.equal(hqq.hqq_linear_backward(dY, w).double(), W)
