@@ -129,7 +129,8 @@ hqqk::MidJob mid_job(int mode, int64_t M, const hqq_weight& w, const hqq_weight*
 //   * from the codes, every token tile converts the weights again: 0.45 ns per thousand codes, and
 //     0.0022 more for each token of the tile;
 //   * dequantized, 0.6 ns per thousand codes to write and read W', then waves of 256 x 256 tiles
-//     over 74 CTA pairs at 0.27 us per 64 of the contraction, and 10 us of launches.
+//     over 74 CTA pairs at 0.27 us per 64 of the contraction (shared by the parts of a product of few
+//     tiles), and 10 or 15 us of launches.
 // Measured in us, 4 bits, 11008 x 4096 (forward) and 4096 x 11008 (gradient), codes / dequantized:
 //   tokens    64        256       512       768       1024
 //   linear    27 / 54   46 / 55   83 / 77  106 / 77  136 / 98
@@ -147,28 +148,39 @@ bool use_mid(int mode, int64_t M, const hqq_weight& w, const hqq_weight* up, siz
   const int64_t out = back ? w.cols : w.rows, inner = back ? w.rows : w.cols;
   const int64_t tile_n = mode == hqqk::kMidGated ? 128 : 256;
   const int64_t tiles = ((M + 255) / 256) * ((out + tile_n - 1) / tile_n);
-  const double dense = 0.6 * codes + 10.0 +
+  const int kind = back ? hqqk::kDenseBackward : up ? hqqk::kDenseGated : hqqk::kDenseForward;
+  const int parts = hqqk::dense_splits(kind, M, out, inner, up ? 2 : 1);
+  const double dense = 0.6 * codes + (parts > 1 ? 15.0 : 10.0) +
                        0.27 * static_cast<double>((tiles + 73) / 74) *
-                           static_cast<double>((inner + 63) / 64) * (back && up ? 2 : 1);
+                           static_cast<double>((inner + 63) / 64) * (back && up ? 2 : 1) / parts;
   if (direct > dense) return false;
   *need = (plan.partial_bytes + 255) / 256 * 256;
   return true;
 }
 
-size_t dense_need(const hqq_weight& w, const hqq_weight* up) {
+// The dequantized weights, then the partial sums of a product of few tiles.
+size_t dense_weights(const hqq_weight& w, const hqq_weight* up) {
   return weight_bytes(w) + (up ? weight_bytes(*up) : 0);
+}
+
+size_t dense_need(int kind, int64_t M, const hqq_weight& w, const hqq_weight* up) {
+  const bool back = kind == hqqk::kDenseBackward;
+  return dense_weights(w, up) + hqqk::dense_partial_bytes(kind, M, back ? w.cols : w.rows,
+                                                          back ? w.rows : w.cols, up ? 2 : 1);
 }
 
 size_t forward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
   size_t need = 0;
   if (M == 0 || w.rows == 0 || w.cols == 0 || use_few(M, w, up)) return 0;
-  return use_mid(up ? hqqk::kMidGated : hqqk::kMidLinear, M, w, up, &need) ? need : dense_need(w, up);
+  if (use_mid(up ? hqqk::kMidGated : hqqk::kMidLinear, M, w, up, &need)) return need;
+  return dense_need(up ? hqqk::kDenseGated : hqqk::kDenseForward, M, w, up);
 }
 
 size_t backward_need(int64_t M, const hqq_weight& w, const hqq_weight* up) {
   size_t need = 0;
   if (M == 0 || w.rows == 0 || w.cols == 0) return 0;
-  return use_mid(hqqk::kMidBackward, M, w, up, &need) ? need : dense_need(w, up);
+  if (use_mid(hqqk::kMidBackward, M, w, up, &need)) return need;
+  return dense_need(hqqk::kDenseBackward, M, w, up);
 }
 
 hqqk::DequantJob dequant_job(const hqq_weight& w, int dtype, void* out) {
@@ -261,6 +273,7 @@ hqq_status forward(const void* X, int64_t M, int dtype, const hqq_weight& w, con
   j.K = w.cols;
   j.x_dtype = dtype;
   j.act = act;
+  j.partial = static_cast<char*>(workspace) + dense_weights(w, up);
   j.D = Y;
   j.G = G;
   j.U = U;
@@ -293,6 +306,7 @@ hqq_status backward(const void* const (&A)[2], int64_t M, int dtype, const hqq_w
   j.N = w.cols;
   j.K = w.rows;
   j.x_dtype = dtype;
+  j.partial = static_cast<char*>(workspace) + dense_weights(w, up);
   j.D = dX;
   return cuda_status(hqqk::launch_dense(j, stream));
 }

@@ -19,6 +19,7 @@
 // are persistent and visit tiles with the row blocks fastest (16 at a time), so that the
 // A panel stays in L2 while each B panel is read once. In the gated form the tile's columns are
 // 128 of the gate (the leader's B) and the same 128 of the up projection (the follower's B).
+// Where tiles are few the contraction is cut into parts, whose sums a second kernel adds in order.
 //
 // Every wait is bounded (about two seconds); on expiry the CTA raises an abort flag, counts the
 // timeout, skips its remaining work, waits (bounded) for its copies in flight and frees its TMEM.
@@ -34,6 +35,7 @@
 #include "hqq_device.cuh"
 #include "hqq_kernels.h"
 #include "hqq_tensor.cuh"
+#include "hqq_tiles.h"
 
 namespace hqqk {
 namespace {
@@ -69,6 +71,10 @@ struct DenseArgs {
   int M, N, K;          // output rows and columns, contraction of one source
   int sources;
   int tiles_m, tiles_n;
+  int splits, kb_split;  // parts of the contraction, k-blocks of a part
+  float* partial;        // of more than one part: [part][products][M][N]
+  unsigned short *D, *G, *U;
+  int act;
   bool save_g, save_u;
 };
 
@@ -91,8 +97,10 @@ __device__ __forceinline__ uint32_t dense_idesc() {
          (static_cast<uint32_t>(dense::kBM >> 4) << 24);
 }
 
-// Tile index -> (row block, column block): row blocks fastest inside bands of kGroupM.
+// Tile index -> (row block, column block): row blocks fastest inside bands of kGroupM. The parts of
+// the contraction follow one another.
 __device__ __forceinline__ void tile_coords(int tile, const DenseArgs& a, int* tm, int* tn) {
+  tile %= a.tiles_m * a.tiles_n;
   const int band = tile / (dense::kGroupM * a.tiles_n);
   const int first = band * dense::kGroupM;
   const int rows = min(dense::kGroupM, a.tiles_m - first);
@@ -145,9 +153,12 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
   const uint32_t rank = cluster_rank();  // 0: leader, issues the MMAs
   const bool leader = rank == 0;
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
-  const int tiles = args.tiles_m * args.tiles_n;
+  const int tiles = args.tiles_m * args.tiles_n * args.splits;
   const int KB1 = (args.K + kBK - 1) / kBK;
   const int KB = KB1 * args.sources;
+  // the k-blocks of a tile's part
+  auto part_begin = [&](int tile) { return tile / (args.tiles_m * args.tiles_n) * args.kb_split; };
+  auto part_end = [&](int tile) { return min(KB, part_begin(tile) + args.kb_split); };
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffAbort);
   auto bar = [&](int i) { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
 
@@ -178,6 +189,9 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
   const uint32_t leader_bars = cluster_addr(sbase + kOffBar, 0);
   auto lbar = [&](int i) { return leader_bars + 8u * static_cast<uint32_t>(i); };
 
+  // dense_finish_kernel may take its place now; it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
     int it = 0;
@@ -187,7 +201,8 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
       tile_coords(tile, args, &tm, &tn);
       const int m0 = tm * kBM + static_cast<int>(rank) * 128;
       const int n0 = tn * kTileN + (KIND == kDenseGated ? 0 : static_cast<int>(rank) * 128);
-      for (int kb = 0; kb < KB; ++kb, ++it) {
+      const int end = part_end(tile);
+      for (int kb = part_begin(tile); kb < end; ++kb, ++it) {
         const int s = it % kStages;
         if (!mbar_wait_cl(bar(kEmpty + s), ((it / kStages) & 1) ^ 1, abort_flag)) {
           go = false;
@@ -231,7 +246,8 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
           const uint32_t acc = n & 1;
           if (!mbar_wait_cl(bar(kAccEmpty + acc), ((n >> 1) & 1) ^ 1, abort_flag)) break;
           tc_fence_after();
-          for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int begin = part_begin(tile), end = part_end(tile);
+          for (int kb = begin; kb < end; ++kb, ++it) {
             const int s = it % kStages;
             if (!mbar_wait_cl(bar(kFull + s), (it / kStages) & 1, abort_flag)) {
               go = false;
@@ -244,13 +260,13 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
               tc_mma_pair(tmem + acc * kBN, da + 2 * k, db + (kMN ? 128 : 2) * k, idesc,
-                          (kb | k) != 0);
+                          kb != begin || k != 0);
             tc_commit_pair(bar(kEmpty + s));
           }
           if (go) tc_commit_pair(bar(kAccFull + acc));
         }
       } else {
-        for (int tile = pair; tile < tiles; tile += pairs) it += KB;
+        for (int tile = pair; tile < tiles; tile += pairs) it += part_end(tile) - part_begin(tile);
       }
       // The commits land in both CTAs' barriers asynchronously: see the last use of every stage
       // completed before the pair parts (a bounded wait; after an abort it may run out).
@@ -285,6 +301,20 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
         const bool in = nc < args.N && row0 < args.M;
         uint32_t r[32], o[16];
         tmem_ld32(base + c * 32, r);
+        if (args.splits > 1) {  // a part: 32 columns of this lane's row, unrounded
+          constexpr int kProducts = KIND == kDenseGated ? 2 : 1;
+          const int64_t part = tile / (args.tiles_m * args.tiles_n), row = row0 + lane;
+#pragma unroll
+          for (int m = 0; m < kProducts; ++m) {
+            if (m == 1) tmem_ld32(base + kTileN + c * 32, r);
+            float* to = args.partial + ((part * kProducts + m) * args.M + row) * args.N + nc;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)  // N is a multiple of 8
+              if (row < args.M && nc + i < args.N)
+                *reinterpret_cast<uint4*>(to + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+          }
+          continue;
+        }
         if constexpr (KIND == kDenseGated) {
           uint32_t r2[32], og[16], ou[16];
           tmem_ld32(base + kTileN + c * 32, r2);
@@ -337,6 +367,53 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
                  : "memory");
+  }
+}
+
+// The parts of a product added in order, then its epilogue; four outputs a thread. Launched while the
+// product runs (programmatic dependent launch); waits for its end first.
+template <bool F16, int KIND>
+__global__ void __launch_bounds__(256, 4) dense_finish_kernel(const DenseArgs a) {
+  constexpr int OUT = F16 ? kF16 : kBF16;
+  constexpr int kProducts = KIND == kDenseGated ? 2 : 1;
+  const int64_t plane = static_cast<int64_t>(a.M) * a.N;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int64_t at = (blockIdx.x * static_cast<int64_t>(256) + threadIdx.x) * 4; at < plane;
+       at += static_cast<int64_t>(gridDim.x) * 1024) {
+    float s[kProducts][4] = {};
+    for (int p = 0; p < a.splits; ++p) {
+#pragma unroll
+      for (int m = 0; m < kProducts; ++m) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + (p * kProducts + m) * plane + at));
+        s[m][0] = __fadd_rn(s[m][0], v.x);
+        s[m][1] = __fadd_rn(s[m][1], v.y);
+        s[m][2] = __fadd_rn(s[m][2], v.z);
+        s[m][3] = __fadd_rn(s[m][3], v.w);
+      }
+    }
+    const int n = static_cast<int>(at % a.N);
+    float y[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      y[q] = s[0][q];
+      if constexpr (KIND != kDenseBackward) y[q] = __fadd_rn(y[q], bias_at<F16>(a.bias[0], n + q, a.N));
+      if constexpr (KIND == kDenseGated) {
+        s[0][q] = y[q];
+        s[1][q] = __fadd_rn(s[1][q], bias_at<F16>(a.bias[1], n + q, a.N));
+        const float h = a.act == kSilu   ? act_f32<kSilu>(y[q])
+                        : a.act == kGelu ? act_f32<kGelu>(y[q])
+                                         : act_f32<kGeluTanh>(y[q]);
+        y[q] = __fmul_rn(h, s[1][q]);
+      }
+    }
+    auto four = [&](unsigned short* to, const float* v) {
+      *reinterpret_cast<uint2*>(to + at) = make_uint2(pack2_16<OUT>(v[0], v[1]), pack2_16<OUT>(v[2], v[3]));
+    };
+    four(a.D, y);
+    if constexpr (KIND == kDenseGated) {
+      if (a.G != nullptr) four(a.G, s[0]);
+      if (a.U != nullptr) four(a.U, s[1]);
+    }
   }
 }
 
@@ -408,10 +485,19 @@ cudaError_t launch_dense_typed(const DenseJob& j, cudaStream_t st) {
   if (tm * tn > 0x3FFFFFFF) return cudaErrorInvalidValue;
   args.tiles_m = static_cast<int>(tm);
   args.tiles_n = static_cast<int>(tn);
+  const int KB = static_cast<int>((j.K + dense::kBK - 1) / dense::kBK) * args.sources;
+  args.splits = dense_splits(j.kind, j.M, j.N, j.K, j.sources);
+  args.kb_split = (KB + args.splits - 1) / args.splits;
+  args.splits = (KB + args.kb_split - 1) / args.kb_split;  // no empty part
+  args.partial = static_cast<float*>(j.partial);
+  args.D = static_cast<unsigned short*>(j.D);
+  args.G = static_cast<unsigned short*>(j.G);
+  args.U = static_cast<unsigned short*>(j.U);
+  args.act = j.act;
   args.save_g = j.G != nullptr;
   args.save_u = j.U != nullptr;
   const int64_t pairs =
-      std::min<int64_t>(tm * tn, resident_pairs(reinterpret_cast<const void*>(kernel)));
+      std::min<int64_t>(tm * tn * args.splits, resident_pairs(reinterpret_cast<const void*>(kernel)));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -424,7 +510,14 @@ cudaError_t launch_dense_typed(const DenseJob& j, cudaStream_t st) {
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(dense::kThreads);
   cfg.dynamicSmemBytes = dense::kSmemBytes;
-  return cudaLaunchKernelEx(&cfg, kernel, a[0], a[1], b[0], b[1], d, g, u, args);
+  e = cudaLaunchKernelEx(&cfg, kernel, a[0], a[1], b[0], b[1], d, g, u, args);
+  if (e != cudaSuccess || args.splits == 1) return e;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((j.M * j.N / 4 + 255) / 256, kSms * 8)));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, dense_finish_kernel<F16, KIND>, args);
 }
 
 template <bool F16>
@@ -548,6 +641,20 @@ __global__ void __launch_bounds__(256)
 }
 
 }  // namespace
+
+// Few tiles leave most pairs idle: as many parts of the contraction as keep them busy, of 16
+// k-blocks at least. (129 tokens, two sources of 11008 x 4096: 16 tiles; 115 us in one part.)
+int dense_splits(int kind, int64_t M, int64_t N, int64_t K, int sources) {
+  const int64_t tile_n = kind == kDenseGated ? dense::kBN / 2 : dense::kBN;
+  const int64_t tiles = ((M + dense::kBM - 1) / dense::kBM) * ((N + tile_n - 1) / tile_n);
+  const int64_t kb = (K + dense::kBK - 1) / dense::kBK * (kind == kDenseBackward ? sources : 1);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms / 2 / tiles, kb / 16)));
+}
+
+size_t dense_partial_bytes(int kind, int64_t M, int64_t N, int64_t K, int sources) {
+  const int splits = dense_splits(kind, M, N, K, sources);
+  return splits == 1 ? 0 : static_cast<size_t>(splits) * (kind == kDenseGated ? 2 : 1) * M * N * sizeof(float);
+}
 
 cudaError_t launch_dense(const DenseJob& j, cudaStream_t st) {
   return j.x_dtype == kF16 ? launch_dense_kind<true>(j, st) : launch_dense_kind<false>(j, st);

@@ -116,7 +116,11 @@ struct DenseJob {
   int x_dtype;
   int act;
   void *D, *G, *U;
+  void* partial;  // dense_partial_bytes of workspace
 };
+// Parts of the contraction a product is cut into, and the workspace their sums take (0 for one part).
+int dense_splits(int kind, int64_t M, int64_t N, int64_t K, int sources);
+size_t dense_partial_bytes(int kind, int64_t M, int64_t N, int64_t K, int sources);
 cudaError_t launch_dense(const DenseJob& job, cudaStream_t stream);
 cudaError_t read_dense_timeouts(unsigned int* out);
 

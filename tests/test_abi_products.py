@@ -131,11 +131,13 @@ def test_workspace_sizes(L):
         assert one(M, 0, nbits=3, cols=72, G=8) == 0
     big = dict(rows=4096, cols=4096)
     assert one(8192, 0, **big) == one(8192, 1, **big) == 2 * 4096 * 4096  # the dequantized weight
-    assert one(1, 0, axis=0, **big) == 2 * 4096 * 4096
+    # few tiles: also the partial sums of four parts of the contraction
+    assert one(1, 0, axis=0, **big) == 2 * 4096 * 4096 + 4 * 4 * 4096
     a, b = weight(**big), weight(nbits=2, G=16, **big)
     size = L.hqq_gated_linear_workspace_bytes
     assert size(1, ctypes.addressof(a), ctypes.addressof(a), 0) == 0
-    assert size(1, ctypes.addressof(a), ctypes.addressof(b), 0) == 4 * 4096 * 4096  # two formats
+    # two formats: both dequantized, and two parts of both products
+    assert size(1, ctypes.addressof(a), ctypes.addressof(b), 0) == 4 * 4096 * 4096 + 2 * 2 * 4 * 4096
     assert size(8192, ctypes.addressof(a), ctypes.addressof(a), 1) == 4 * 4096 * 4096
     assert 0 < one(64, 0, **big) < 2 * 4096 * 4096   # partial sums only
     assert one(-1, 0) == one(1 << 31, 0) == ctypes.c_size_t(-1).value

@@ -286,6 +286,28 @@ def test_many_tokens_along_the_rows(M, N, K):
     close(dX, dY64[rows] @ gate.W, N * 2.0 ** -23 * (np.abs(dY64[rows]) @ np.abs(gate.W)), "bf16", "dX")
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 264, 4104), (129, 520, 2304), (300, 72, 8192)])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_few_tiles_of_a_long_contraction(M, N, K, act):
+    """Products on dequantized weights whose contraction is cut into parts."""
+    gate = Layer(N, K, 4, 8, 0, "bf16", bias=True, seed=M)
+    up = Layer(N, K, 2, 8, 0, "bf16", seed=M + 1)
+    X, X64 = draw((M, K), M, "bf16", scale=0.5 / np.sqrt(K) / np.abs(gate.W).max())
+    check_gated(M, N, K, act, "bf16", gate, up, X, X64)
+    S, e = gate.project(X64)
+    close(host(hqq.hqq_linear_ex(X, gate.h)), S, e, "bf16", "Y")
+    gate, up = (Layer(K, N, 4, 8, 0, "bf16", seed=M + s) for s in (2, 3))  # gradients contract over K
+    dY, _ = draw((M, K), 1, "bf16")
+    g, _ = draw((M, K), 2, "bf16")
+    u, _ = draw((M, K), 3, "bf16")
+    dX, dG, dU = hqq.hqq_gated_linear_backward(dY, g, u, gate.h, up.h, act)
+    rG, rU = host(dG), host(dU)
+    S = np.abs(rG) @ np.abs(gate.W) + np.abs(rU) @ np.abs(up.W)
+    close(host(dX), rG @ gate.W + rU @ up.W, 2 * K * 2.0 ** -23 * S, "bf16", "dX")
+    e = K * 2.0 ** -23 * (np.abs(host(dY)) @ np.abs(gate.W))
+    close(host(hqq.hqq_linear_backward(dY, gate.h)), host(dY) @ gate.W, e, "bf16", "dX of one weight")
+
+
 # ------------------------------------------------------------------ odd scales and zeros
 
 @pytest.mark.parametrize("nbits", NBITS)
