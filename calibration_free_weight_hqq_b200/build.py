@@ -21,7 +21,7 @@ SOURCES = ["hqq_abi.cu", "hqq_quantize.cu", "hqq_quantize_stop.cu", "hqq_dequant
            "hqq_noalloc.cu", "hqq_gemm.cu", "hqq_mx.cu", "hqq_abi_product.cu", "hqq_few.cu",
            "hqq_few_1.cu", "hqq_few_2.cu", "hqq_few_3.cu", "hqq_few_4.cu", "hqq_few_8.cu",
            "hqq_mid.cu", "hqq_mid_1.cu", "hqq_mid_2.cu", "hqq_mid_3.cu", "hqq_mid_4.cu",
-           "hqq_mid_8.cu", "hqq_dense.cu"]
+           "hqq_mid_8.cu", "hqq_columns.cu", "hqq_dense.cu"]
 HEADERS = ["hqq_device.cuh", "hqq_tensor.cuh", "hqq_act.cuh", "hqq_kernels.h",
            "hqq_quantize_impl.cuh", "hqq_tiles.h", "hqq_codes.cuh", "hqq_few.h",
            "hqq_few_impl.cuh", "hqq_mid.h", "hqq_mid_impl.cuh", "hqq_abi_internal.h"]

@@ -204,18 +204,20 @@ hqqk::DequantJob dequant_job(const hqq_weight& w, int dtype, void* out) {
   return j;
 }
 
+hqq_status dequantize_one(const hqqk::DequantJob& j, cudaStream_t stream) {
+  return cuda_status(hqqk::columns_serve(j) ? hqqk::launch_columns(j, stream)
+                                            : hqqk::launch_dequantize(j, stream));
+}
+
 // The weight, or both of a pair, dequantized into the workspace, one after the other: W'[i] in
 // out[i].
 hqq_status dequantize_into(void* workspace, const hqq_weight& w, const hqq_weight* up, int dtype,
                            const void* (&out)[2], cudaStream_t stream) {
   out[0] = workspace;
   out[1] = static_cast<char*>(workspace) + (up ? weight_bytes(w) : 0);
-  hqq_status st = cuda_status(
-      hqqk::launch_dequantize(dequant_job(w, dtype, const_cast<void*>(out[0])), stream));
-  if (st == HQQ_OK && up)
-    st = cuda_status(
-        hqqk::launch_dequantize(dequant_job(*up, dtype, const_cast<void*>(out[1])), stream));
-  return st;
+  const hqq_status st = dequantize_one(dequant_job(w, dtype, const_cast<void*>(out[0])), stream);
+  if (st != HQQ_OK || !up) return st;
+  return dequantize_one(dequant_job(*up, dtype, const_cast<void*>(out[1])), stream);
 }
 
 hqq_status check_workspace(const void* workspace, size_t bytes, size_t need) {

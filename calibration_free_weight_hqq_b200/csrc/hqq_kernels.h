@@ -124,6 +124,11 @@ size_t dense_partial_bytes(int kind, int64_t M, int64_t N, int64_t K, int source
 cudaError_t launch_dense(const DenseJob& job, cudaStream_t stream);
 cudaError_t read_dense_timeouts(unsigned int* out);
 
+// Dequantization of an axis-0 weight of 8 | cols to 16 bits, for long groups and 3-bit codes
+// (columns_serve); values as launch_dequantize writes them.
+bool columns_serve(const DequantJob& job);
+cudaError_t launch_columns(const DequantJob& job, cudaStream_t stream);
+
 // Products over weights of no columns: every sum is its bias (or 0).
 cudaError_t launch_empty_sums(const void* const (&bias)[2], int mats, int64_t M, int64_t N,
                               int x_dtype, int act, void* Y, void* G, void* U,

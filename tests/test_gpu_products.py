@@ -154,6 +154,19 @@ def test_one_hot_backward_is_the_dequantized_weight(nbits, G, axis, meta):
     assert np.array_equal(host(hqq.hqq_linear_backward(eye, L.h)), L.W)
 
 
+@pytest.mark.parametrize("K", [8, 136, 264])
+@pytest.mark.parametrize("G,meta,dtype", [(16, "f16", "bf16"), (32, "u8", "f16"), (64, "f32", "f16"),
+                                          (128, "u8scale", "bf16"), (256, "u8zero", "f16")])
+@pytest.mark.parametrize("nbits", NBITS)
+def test_one_hot_of_groups_down_the_columns(nbits, G, meta, dtype, K):
+    N = 3 * G
+    L = Layer(N, K, nbits, G, 0, dtype, meta, seed=nbits + G + K)
+    eye = torch.eye(K, dtype=TORCH[dtype], device="cuda")
+    assert np.array_equal(host(hqq.hqq_linear_ex(eye, L.h)), L.W.T)
+    eye = torch.eye(N, dtype=TORCH[dtype], device="cuda")
+    assert np.array_equal(host(hqq.hqq_linear_backward(eye, L.h)), L.W)
+
+
 # ------------------------------------------------------------------ random products
 
 SIZES = [(1, 8, 8), (1, 4096, 1024), (2, 264, 320), (7, 40, 72), (8, 1000, 2048), (9, 136, 1096),
