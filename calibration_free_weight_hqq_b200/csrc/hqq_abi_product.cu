@@ -125,34 +125,43 @@ hqqk::MidJob mid_job(int mode, int64_t M, const hqq_weight& w, const hqq_weight*
 }
 
 // Whether a product runs straight from the codes on the some-token kernel rather than on dequantized
-// weights, and what workspace that takes. Both times in us are estimated from the sizes:
-//   * from the codes, every token tile converts the weights again: 0.45 ns per thousand codes, and
-//     0.0022 more for each token of the tile;
-//   * dequantized, 0.6 ns per thousand codes to write and read W', then waves of 256 x 256 tiles
-//     over 74 CTA pairs at 0.27 us per 64 of the contraction (shared by the parts of a product of few
-//     tiles), and 10 or 15 us of launches.
-// Measured in us, 4 bits, 11008 x 4096 (forward) and 4096 x 11008 (gradient), codes / dequantized:
-//   tokens    64        256       512       768       1024
-//   linear    27 / 54   46 / 55   83 / 77  106 / 77  136 / 98
-//   gradient  28 / 52   48 / 53   85 / 73  109 / 74  140 / 94
-//   gated     48 / 113  81 / 114 169 / 133 217 / 154 309 / 175
-//   its grad. 50 / 162  72 / 166 113 / 171 158 / 175 215 / 183
+// weights, and what workspace that takes. Both times in us are estimated from the sizes, in millions of
+// codes, partial sums and outputs:
+//   * from the codes: every token tile converts the weights again, 0.26 us for a million codes and
+//     0.0007 more for each token of the tile (3-bit codes 1.4 times that), then the partial sums;
+//   * dequantized: 0.57 us for a million codes, then waves of 256 x 256 tiles over 74 CTA pairs at
+//     0.33 us for 64 of the contraction, and the partial sums of a product of few tiles.
+// The constants fit 480 pairs of measured times (four products, weights of 4096 x 4096, 4096 x 11008,
+// 11008 x 4096 and 1024 x 8192, 1 to 8 bits, 24 to 768 tokens) to 9 % and 5 %; the route taken is on
+// average 0.5 % slower than the better one. Measured in us, 4 bits, 11008 x 4096 forward and
+// 4096 x 11008 backward for the first two rows, 11008 x 4096 for the others, codes / dequantized:
+//   tokens       64        256         333         512         768
+//   linear       24 / 50   43 / 50     62 / 72     80 / 73   102 / 74
+//   gradient     25 / 48   44 / 49     63 / 69     81 / 70   105 / 71
+//   gated        44 / 106  77 / 107   134 / 124   167 / 126  214 / 147
+//   its grad.    42 / 89   64 / 97     90 / 120   110 / 125  159 / 169
 bool use_mid(int mode, int64_t M, const hqq_weight& w, const hqq_weight* up, size_t* need) {
   if (w.params.axis != 1) return false;
   if (up != nullptr && !same_format(w.params, up->params)) return false;
   hqqk::MidPlan plan;
   if (!hqqk::mid_plan(mid_job(mode, M, w, up), &plan)) return false;
-  const bool back = mode == hqqk::kMidBackward;
-  const double codes = 1e-6 * static_cast<double>(w.rows) * static_cast<double>(w.cols) * (up ? 2 : 1);
-  const double direct = codes * plan.tok_tiles * (0.45 + 0.0022 * plan.tok);
+  const bool back = mode == hqqk::kMidBackward, gated = mode == hqqk::kMidGated;
+  const double pair = up ? 1.0 : 0.0;
+  const double codes = 1e-6 * static_cast<double>(w.rows) * static_cast<double>(w.cols) * (1 + pair);
   const int64_t out = back ? w.cols : w.rows, inner = back ? w.rows : w.cols;
-  const int64_t tile_n = mode == hqqk::kMidGated ? 128 : 256;
+  const double sums = 1e-6 * static_cast<double>(M) * static_cast<double>(out) * (gated ? 2 : 1);
+  const double held = 1e-6 * plan.ctas * 2 * plan.tok * hqqk::kMidRows * (gated ? 2 : 1);
+  const double direct = 8.5 + 2.2 * pair + 1.05 * held + 2.1 * sums +
+                        codes * plan.tok_tiles * (0.26 + 0.0007 * plan.tok) *
+                            (w.params.nbits == 3 ? 1.4 : 1.0);
+  const int64_t tile_n = gated ? 128 : 256;
   const int64_t tiles = ((M + 255) / 256) * ((out + tile_n - 1) / tile_n);
+  const int64_t kb = (inner + 63) / 64 * (back && up ? 2 : 1);
   const int kind = back ? hqqk::kDenseBackward : up ? hqqk::kDenseGated : hqqk::kDenseForward;
   const int parts = hqqk::dense_splits(kind, M, out, inner, up ? 2 : 1);
-  const double dense = 0.6 * codes + (parts > 1 ? 15.0 : 10.0) +
-                       0.27 * static_cast<double>((tiles + 73) / 74) *
-                           static_cast<double>((inner + 63) / 64) * (back && up ? 2 : 1) / parts;
+  const double dense = 6.4 + 3.6 * pair + 0.57 * codes + (parts > 1 ? 1.8 * parts * sums : 0.0) +
+                       0.33 * static_cast<double>((tiles * parts + 73) / 74) *
+                           static_cast<double>((kb + parts - 1) / parts);
   if (direct > dense) return false;
   *need = (plan.partial_bytes + 255) / 256 * 256;
   return true;
