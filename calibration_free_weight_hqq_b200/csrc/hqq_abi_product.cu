@@ -128,7 +128,7 @@ hqqk::MidJob mid_job(int mode, int64_t M, const hqq_weight& w, const hqq_weight*
 // weights, and what workspace that takes. Both times in us are estimated from the sizes, in millions of
 // codes, partial sums and outputs:
 //   * from the codes: every token tile converts the weights again, 0.26 us for a million codes and
-//     0.0007 more for each token of the tile (3-bit codes 1.4 times that), then the partial sums;
+//     0.0007 more for each token of the tile, then the partial sums;
 //   * dequantized: 0.57 us for a million codes, then waves of 256 x 256 tiles over 74 CTA pairs at
 //     0.33 us for 64 of the contraction, and the partial sums of a product of few tiles.
 // The constants fit 480 pairs of measured times (four products, weights of 4096 x 4096, 4096 x 11008,
@@ -152,8 +152,7 @@ bool use_mid(int mode, int64_t M, const hqq_weight& w, const hqq_weight* up, siz
   const double sums = 1e-6 * static_cast<double>(M) * static_cast<double>(out) * (gated ? 2 : 1);
   const double held = 1e-6 * plan.ctas * 2 * plan.tok * hqqk::kMidRows * (gated ? 2 : 1);
   const double direct = 8.5 + 2.2 * pair + 1.05 * held + 2.1 * sums +
-                        codes * plan.tok_tiles * (0.26 + 0.0007 * plan.tok) *
-                            (w.params.nbits == 3 ? 1.4 : 1.0);
+                        codes * plan.tok_tiles * (0.26 + 0.0007 * plan.tok);
   const int64_t tile_n = gated ? 128 : 256;
   const int64_t tiles = ((M + 255) / 256) * ((out + tile_n - 1) / tile_n);
   const int64_t kb = (inner + 63) / 64 * (back && up ? 2 : 1);

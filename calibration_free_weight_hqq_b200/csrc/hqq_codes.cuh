@@ -30,7 +30,7 @@ struct WeightArgs {
 };
 
 // The codes of 32 consecutive elements: 32-bit words, least significant code first (8, 4, 2, 1 bits:
-// NBITS words); 3 bits: one 24-bit field of 8 codes per word.
+// NBITS words); 3 bits: ten to a word, whose bits 30 and 31 hold anything, as do those past the last.
 template <int NBITS>
 struct Codes32 {
   static constexpr int kWords = NBITS == 3 ? 4 : NBITS;
@@ -41,16 +41,21 @@ struct Codes32 {
 // stand: at bits 0 .. of a half under 1024 they read 1024 + q, at bits NBITS .. under
 // 2^(10 - NBITS) they read that plus q, exactly; one shift serves two masks, and each mask takes two
 // codes, 16 bits apart. Pair p of unit u (8 MMA k slots) holds the elements
-//   8 and 3 bits  8u + 2p, 8u + 2p + 1            2 bits  16(u/2) + 4(u%2) + p, 8 further
+//   8 bits        8u + 2p, 8u + 2p + 1            2 bits  16(u/2) + 4(u%2) + p, 8 further
 //   4 bits        8u + p, 8u + p + 4              1 bit   4u + p, 16 further
-// of its chunk of 32, and X is laid out in the same order (slot_element).
+// of its chunk of 32, and X is laid out in the same order (slot_element). At 3 bits, codes five apart
+// in a word stand 15 bits apart: with the first at bits 1 .. 3, under 512, the second is at bits 0 ..
+// 2 of its half, under 1024. Pair i = 4u + p holds 10(i/5) + i%5 and the one 5 further, the last
+// pair the last two codes.
 template <int NBITS>
 __host__ __device__ constexpr int slot_element(int u, int j) {  // slot j = 0 .. 7 of unit u
   const int p = j / 2, h = j % 2;
   return NBITS == 4   ? 8 * u + p + 4 * h
          : NBITS == 2 ? 16 * (u / 2) + 4 * (u % 2) + p + 8 * h
          : NBITS == 1 ? 4 * u + p + 16 * h
-                      : 8 * u + j;
+         : NBITS == 8 ? 8 * u + j
+         : 4 * u + p == 15 ? 30 + h
+                           : (4 * u + p) / 5 * 10 + (4 * u + p) % 5 + 5 * h;
 }
 // (v & mask) | bits in one instruction.
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
@@ -58,10 +63,14 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
   return d;
 }
-// The base under a code of pair p.
+// Whether a code, the first (h 0) or second of pair p, stands under 1024, and the other base.
 template <int NBITS>
-__host__ __device__ constexpr float slot_base(int p) {
-  return NBITS == 8 || NBITS == 3 || p % 2 == 0 ? 1024.0f : static_cast<float>(1 << (10 - NBITS % 8));
+__host__ __device__ constexpr bool under_1024(int p, int h) {
+  return NBITS == 8 || (NBITS == 3 ? h == 1 : p % 2 == 0);
+}
+template <int NBITS>
+__host__ __device__ constexpr float lesser_base() {
+  return NBITS == 8 ? 1024.0f : NBITS == 3 ? 512.0f : static_cast<float>(1 << (10 - NBITS % 8));
 }
 template <int NBITS>
 __device__ __forceinline__ uint32_t widened_pair(const Codes32<NBITS>& c, int u, int p) {
@@ -69,9 +78,11 @@ __device__ __forceinline__ uint32_t widened_pair(const Codes32<NBITS>& c, int u,
   if constexpr (NBITS == 8) {
     return __byte_perm(c.w[2 * u + p / 2], k1024, p % 2 ? 0x5352 : 0x5150);
   } else if constexpr (NBITS == 3) {
-    const uint32_t f = c.w[u];
-    const int hi = 6 * p + 3 - 16;  // the second code's way to bit 16
-    return and_or(hi < 0 ? f << -hi : f >> hi, 0x00070000u, and_or(f >> (6 * p), 7u, k1024));
+    constexpr uint32_t kBases = 0x64006000u;  // 1024 over 512
+    const int i = 4 * u + p, r = i % 5;
+    const uint32_t f = c.w[i / 5];
+    if (i == 15) return and_or(f << 13, 0x00070000u, and_or(f << 1, 0x0000000Eu, kBases));
+    return and_or(r == 0 ? f << 1 : f >> (3 * r - 1), 0x0007000Eu, kBases);
   } else {
     constexpr uint32_t kMask = ((1u << NBITS) - 1u) * 0x00010001u;
     constexpr uint32_t kOdd = k1024 - static_cast<uint32_t>(NBITS) * 0x04000400u;  // 2^(10 - NBITS)
@@ -93,18 +104,18 @@ __device__ __forceinline__ float2 add_f32_f16x2(uint32_t h, float2 c) {
 }
 
 // A group's scale and zero as the conversion takes them. Where base + zero is exact,
-// (base + q) - (base + zero) is the one rounding of q - zero (`even`, `odd` alone, by the pair's
-// base); otherwise the base is subtracted first, exactly, and then zero. If 1024 + zero is exact, so
+// (base + q) - (base + zero) is the one rounding of q - zero (`over_1024`, `over_lesser` alone, by the
+// code's base); otherwise the base is subtracted first, exactly, and then zero. If 1024 + zero is exact, so
 // is the sum with the smaller base. The test is cheap and, for zeros of 8 or 11 significant bits,
 // fails only next to 0.
 struct GroupMeta {
-  float scale, even, odd, neg_zero;
+  float scale, over_1024, over_lesser, neg_zero;
 };
 template <int NBITS>
 __device__ __forceinline__ GroupMeta group_meta(float scale, float zero, bool* one) {
   const float sum = __fadd_rn(zero, 1024.0f);
   *one = *one && __fsub_rn(sum, 1024.0f) == zero;
-  return GroupMeta{scale, -sum, -__fadd_rn(zero, slot_base<NBITS>(1)), -zero};
+  return GroupMeta{scale, -sum, -__fadd_rn(zero, lesser_base<NBITS>()), -zero};
 }
 
 // Pair p of unit u as W' in fp32, with the dequantizer's first two roundings: q - zero, * scale. m: the
@@ -117,10 +128,13 @@ __device__ __forceinline__ float2 dequant_pair(const Codes32<NBITS>& c, int u, i
   const uint32_t h = widened_pair<NBITS>(c, u, p);
   float2 v;
   if constexpr (ONE)
-    v = add_f32_f16x2(h, p % 2 ? make_float2(a.odd, b.odd) : make_float2(a.even, b.even));
+    v = add_f32_f16x2(h, make_float2(under_1024<NBITS>(p, 0) ? a.over_1024 : a.over_lesser,
+                                     under_1024<NBITS>(p, 1) ? b.over_1024 : b.over_lesser));
   else
-    v = fadd2_rn(add_f32_f16x2(h, make_float2(-slot_base<NBITS>(p), -slot_base<NBITS>(p))),
-                 make_float2(a.neg_zero, b.neg_zero));
+    v = fadd2_rn(
+        add_f32_f16x2(h, make_float2(under_1024<NBITS>(p, 0) ? -1024.0f : -lesser_base<NBITS>(),
+                                     under_1024<NBITS>(p, 1) ? -1024.0f : -lesser_base<NBITS>())),
+        make_float2(a.neg_zero, b.neg_zero));
   return fmul2_rn(v, make_float2(a.scale, b.scale));
 }
 
@@ -143,25 +157,17 @@ __device__ __forceinline__ void dequant_chunk(const Codes32<NBITS>& c, const Gro
   float2 v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = dequant_pair<NBITS, GROUPS, ONE>(c, i / 4, i % 4, m);
-  auto four = [](float2 a, float2 b, float2 c, float2 d) {
-    return make_uint4(pack2_16<OUT>(a.x, a.y), pack2_16<OUT>(b.x, b.y), pack2_16<OUT>(c.x, c.y),
-                      pack2_16<OUT>(d.x, d.y));
-  };
-  auto lows = [&](int i) { return make_float2(v[i].x, v[i + 1].x); };
-  auto highs = [&](int i) { return make_float2(v[i].y, v[i + 1].y); };
+  float e[32];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if constexpr (NBITS == 4)
-      o[u] = four(lows(4 * u), lows(4 * u + 2), highs(4 * u), highs(4 * u + 2));
-    else if constexpr (NBITS == 2)
-      o[u] = u % 2 == 0 ? four(lows(4 * u), lows(4 * u + 2), lows(4 * u + 4), lows(4 * u + 6))
-                        : four(highs(4 * u - 4), highs(4 * u - 2), highs(4 * u), highs(4 * u + 2));
-    else if constexpr (NBITS == 1)
-      o[u] = u < 2 ? four(lows(8 * u), lows(8 * u + 2), lows(8 * u + 4), lows(8 * u + 6))
-                   : four(highs(8 * u - 16), highs(8 * u - 14), highs(8 * u - 12), highs(8 * u - 10));
-    else
-      o[u] = four(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+  for (int i = 0; i < 16; ++i) {
+    e[slot_element<NBITS>(i / 4, 2 * (i % 4))] = v[i].x;
+    e[slot_element<NBITS>(i / 4, 2 * (i % 4) + 1)] = v[i].y;
   }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    o[u] = make_uint4(pack2_16<OUT>(e[8 * u], e[8 * u + 1]), pack2_16<OUT>(e[8 * u + 2], e[8 * u + 3]),
+                      pack2_16<OUT>(e[8 * u + 4], e[8 * u + 5]),
+                      pack2_16<OUT>(e[8 * u + 6], e[8 * u + 7]));
 }
 
 template <int BYTES>
@@ -170,6 +176,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+// 16 bytes, of which the first `bytes` are read and the others become 0.
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -184,7 +194,8 @@ __device__ __forceinline__ void cp_async_wait() {
 // touched a sector or two per lane and filled the L1's data path: 32 wavefronts a copy.) The pieces
 // of a row are permuted by its number so that reads are free of bank conflicts, for eight lanes that
 // read the same piece of eight rows (QUADS false) or chunks 0, 2, 4, 6 of two rows (QUADS true).
-// Except at 3 bits, rows must start on 16-byte boundaries.
+// Rows must start on 16-byte boundaries, except at 3 bits, where a row's copy starts at the boundary
+// below its first code: pieces of 40 codes, not permuted, the rows an odd number of pieces apart.
 template <int NBITS, int CODES, bool QUADS>
 struct CodeTile {
   static constexpr int kRow = tile_row_bytes(NBITS, CODES);
@@ -199,18 +210,22 @@ struct CodeTile {
   }
 
   // The first `rows` rows and `codes` codes of each. src: the first code's byte, rows `stride` bytes
-  // apart; at 3 bits the word from which `first` counts the first code, rows `stride` codes apart.
+  // apart; at 3 bits the 16-byte boundary from which `first` counts the first code, rows `stride` codes
+  // apart.
   static __device__ __forceinline__ void copy(uint32_t to, const uint8_t* src, uint32_t first,
                                               uint32_t stride, uint32_t rows, uint32_t codes,
                                               uint32_t lane) {
     if constexpr (NBITS == 3) {
-      constexpr uint32_t kWords = kRow / 4;
-#pragma unroll 4
-      for (uint32_t i = lane; i < 16 * kWords; i += 32) {
-        const uint32_t row = i / kWords, word = i - row * kWords;
-        const uint32_t e = first + row * stride, w0 = e / 10u;
-        if (row < rows && 10u * word <= e - 10u * w0 + codes - 1)  // a code of the row is in the word
-          cp_async<4>(to + i * 4, src + (w0 + word) * 4u);
+      constexpr uint32_t kMost = (39 + CODES - 1) / 40 + 1;  // pieces a row may span
+#pragma unroll
+      for (uint32_t n = 0; n < (16 * kMost + 31) / 32; ++n) {
+        const uint32_t i = n * 32 + lane, row = i / kMost, piece = i - row * kMost;
+        const uint32_t e = first + row * stride, p0 = e / 40u;
+        // bytes up to the row's last word; nothing further is read
+        const int left = static_cast<int>((e - 40u * p0 + codes - 1) / 10u * 4u + 4u - 16u * piece);
+        if (row < rows && left > 0)
+          cp_async_part(to + row * kRow + piece * 16, src + (p0 + piece) * 16u,
+                        static_cast<uint32_t>(min(left, 16)));
       }
     } else {
       constexpr uint32_t kAll = 16 * kPieces;
@@ -225,7 +240,7 @@ struct CodeTile {
   }
 
   // The 32 codes of `row` from code `at` (a multiple of 32) on; at 3 bits, slot: the first code of
-  // the row's place in its word.
+  // the row's place in its 16 bytes.
   static __device__ __forceinline__ Codes32<NBITS> read(const uint8_t* tile, uint32_t row, uint32_t at,
                                                         uint32_t slot) {
     Codes32<NBITS> c;
@@ -237,16 +252,10 @@ struct CodeTile {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = p[i];
       v[4] = first_slot == 9 ? p[4] : 0u;  // 31 codes further: the fifth word only from slot 9
+      const uint32_t mask = 0x3FFFFFFFu >> (3 * first_slot);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int here = first_slot + 8 * u;  // 8u .. 8u + 9
-        const int word0 = 8 * u / 10;         // the word of code 8u, or the next one
-        const bool next = here >= 10 * (word0 + 1);
-        const int s = here - 10 * (word0 + (next ? 1 : 0));
-        const uint32_t lo = next ? v[word0 + 1] : v[word0];
-        const uint32_t hi = next ? v[word0 + 2 < 5 ? word0 + 2 : 4] : v[word0 + 1];
-        c.w[u] = (lo & 0x3FFFFFFFu) >> (3 * s) | hi << (30 - 3 * s);
-      }
+      for (int i = 0; i < 4; ++i)
+        c.w[i] = and_or(v[i] >> (3 * first_slot), mask, v[i + 1] << (30 - 3 * first_slot));
     } else {
       const uint32_t byte = at / 8 * NBITS;
       const uint8_t* line = tile + row * kRow;
@@ -279,14 +288,15 @@ inline bool whole_rows(int nbits, int64_t cols) {
   return cols % 32 == 0 && (nbits == 3 || cols / 8 * nbits % 16 == 0);
 }
 
-// A lane's chunk straight from memory, for rows of any multiple of 8 codes, in units of 8 codes (NBITS bytes, aligned to their
-// size): the first `units` of the chunk exist, the others read as code 0.
+// A lane's chunk straight from memory, for rows of any multiple of 8 codes, in units of 8 codes (NBITS
+// bytes, aligned to their size): the first `units` of the chunk exist, the others read as code 0.
 template <int NBITS>
 __device__ __forceinline__ Codes32<NBITS> load_codes_units(const uint8_t* slab, uint32_t e,
                                                            int units) {
   Codes32<NBITS> c;
 #pragma unroll
   for (int i = 0; i < Codes32<NBITS>::kWords; ++i) c.w[i] = 0u;
+  uint32_t f[4] = {0u, 0u, 0u, 0u};  // 3 bits: the units
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if (u >= units) break;
@@ -296,7 +306,7 @@ __device__ __forceinline__ Codes32<NBITS> load_codes_units(const uint8_t* slab, 
       const uint32_t* p = reinterpret_cast<const uint32_t*>(slab) + word;
       const uint32_t lo = __ldg(p) & 0x3FFFFFFFu;
       const uint32_t hi = s > 2 ? __ldg(p + 1) : 0u;  // 8 codes from slot 2 end in this word
-      c.w[u] = lo >> (3 * s) | hi << (30 - 3 * s);
+      f[u] = (lo >> (3 * s) | hi << (30 - 3 * s)) & 0x00FFFFFFu;
     } else {
       const uint8_t* p = slab + static_cast<uint64_t>((e / 8u + u) * NBITS);
       if constexpr (NBITS == 8) {
@@ -313,15 +323,21 @@ __device__ __forceinline__ Codes32<NBITS> load_codes_units(const uint8_t* slab, 
       }
     }
   }
+  if constexpr (NBITS == 3) {
+    c.w[0] = f[0] | f[1] << 24;
+    c.w[1] = f[1] >> 6 | f[2] << 18;
+    c.w[2] = f[2] >> 12 | f[3] << 12;
+    c.w[3] = f[3] >> 18;
+  }
   return c;
 }
 
 // Consecutive rows of one weight: their codes and meta, addressed by 32-bit offsets from here.
 struct Slab {
-  const uint8_t* codes;   // the first code's byte; at 3 bits the word that holds it
+  const uint8_t* codes;   // the first code's byte; at 3 bits the 16-byte boundary below it
   const uint8_t *scale, *zero;
   const float2 *scale_mm, *zero_mm;  // from the run of the slab's first group on, or nullptr
-  uint32_t code0;         // 3 bits: slot of the slab's first code in its word
+  uint32_t code0;         // 3 bits: the first code's place from there, under 40
   uint32_t group0;        // the first group's place in its run
 };
 
@@ -332,8 +348,8 @@ __device__ __forceinline__ Slab slab_of_row(const WeightArgs& a, int i, int64_t 
   const int64_t e0 = row * K, g0 = row * groups_per_row;
   const uint32_t msz = ANY && a.meta_dt == kF32 ? 4 : 2;
   Slab b;
-  b.code0 = NBITS == 3 ? static_cast<uint32_t>(e0 % 10) : 0u;
-  b.codes = a.packed[i] + (NBITS == 3 ? e0 / 10 * 4 : e0 / 8 * NBITS);
+  b.code0 = NBITS == 3 ? static_cast<uint32_t>(e0 % 40) : 0u;
+  b.codes = a.packed[i] + (NBITS == 3 ? e0 / 40 * 16 : e0 / 8 * NBITS);
   b.scale_mm = b.zero_mm = nullptr;
   b.group0 = 0;
   if constexpr (ANY) {

@@ -236,13 +236,13 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
               m[i][r][u] = group_meta<NBITS>(sz.x, sz.y, &one);
             }
         one = !ANY && __all_sync(0xFFFFFFFFu, one);
-        uint32_t slot[MATS][2];  // 3 bits: the first code's place in its word, of both rows
+        uint32_t slot[MATS][2];  // 3 bits: the first code's place in its 16 bytes, of both rows
 #pragma unroll
         for (int i = 0; i < MATS; ++i) {
           slot[i][0] = slot[i][1] = 0u;
           if constexpr (NBITS == 3) {
-            slot[i][0] = (slab[i].code0 + g * K + kb * kFewKB) % 10u;
-            slot[i][1] = (slab[i].code0 + (g + 8) * K + kb * kFewKB) % 10u;
+            slot[i][0] = (slab[i].code0 + g * K + kb * kFewKB) % 40u;
+            slot[i][1] = (slab[i].code0 + (g + 8) * K + kb * kFewKB) % 40u;
           }
         }
         // the next k-block's meta, of the next tile after this one's last

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       return false;
     };
 
-    // codes: where the warp's 16 rows begin (3 bits: the word) in either weight of a stage
+    // codes: where the warp's 16 rows begin (3 bits: the 16-byte boundary below) in either weight of a stage
     Walk cw{};
     const uint8_t* copy_base[MATS];
     uint32_t copy_code0[MATS];
@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       const int64_t e0 = static_cast<int64_t>(cw.row + 16 * wi) * cols;
 #pragma unroll
       for (int i = 0; i < MATS; ++i) {
-        copy_base[i] = a.w.packed[MATS == 2 ? i : cw.mat] + (NBITS == 3 ? e0 / 10 * 4 : e0 / 8 * NBITS);
-        copy_code0[i] = NBITS == 3 ? static_cast<uint32_t>(e0 % 10) : 0u;
+        copy_base[i] = a.w.packed[MATS == 2 ? i : cw.mat] + (NBITS == 3 ? e0 / 40 * 16 : e0 / 8 * NBITS);
+        copy_code0[i] = NBITS == 3 ? static_cast<uint32_t>(e0 % 40) : 0u;
       }
     };
     const int64_t codes_down = static_cast<int64_t>(2 * kBK) * cols / 8 * NBITS;  // two k-blocks of rows
@@ -402,10 +402,10 @@ __global__ void __launch_bounds__(kMidThreads, 1)
             m[h][u] = group_meta<NBITS>(sz.x, sz.y, &one);
           }
         one = !ANY && __all_sync(0xFFFFFFFFu, one);
-        uint32_t first_slot[MATS];  // 3 bits: the row's first code's place in its word
+        uint32_t first_slot[MATS];  // 3 bits: the row's first code's place in its 16 bytes
 #pragma unroll
         for (int i = 0; i < MATS; ++i)
-          first_slot[i] = NBITS == 3 ? (slab[i].code0 + codes0 - cc) % 10u : 0u;
+          first_slot[i] = NBITS == 3 ? (slab[i].code0 + codes0 - cc) % 40u : 0u;
         step_meta();
         fetch_meta();
         cp_async_wait<kDepth - 1>();
