@@ -369,7 +369,8 @@ HQQ_EXPORT hqq_status hqq_linear_backward(const void* dY, int64_t M, hqq_dtype x
   const void* A[2] = {dY, nullptr};
   if ((st = backward(A, M, x_dtype, *w, nullptr, dX, workspace, stream)) != HQQ_OK) return st;
   if (!sums) return HQQ_OK;
-  return cuda_status(hqqk::launch_column_sum(dY, M, w->rows, x_dtype, dbias, stream));
+  return cuda_status(
+      hqqk::launch_column_sums(dY, dbias, nullptr, nullptr, M, w->rows, x_dtype, stream));
 }
 
 HQQ_EXPORT hqq_status hqq_gated_linear_backward(const void* dY, const void* G, const void* U,
@@ -399,9 +400,7 @@ HQQ_EXPORT hqq_status hqq_gated_linear_backward(const void* dY, const void* G, c
   if (st != HQQ_OK) return st;
   const void* A[2] = {dG, dU};
   if ((st = backward(A, M, x_dtype, *gate, up, dX, workspace, stream)) != HQQ_OK) return st;
-  if (N > 0 && dbias_gate)
-    st = cuda_status(hqqk::launch_column_sum(dG, M, N, x_dtype, dbias_gate, stream));
-  if (st == HQQ_OK && N > 0 && dbias_up)
-    st = cuda_status(hqqk::launch_column_sum(dU, M, N, x_dtype, dbias_up, stream));
-  return st;
+  if (!sums) return HQQ_OK;
+  return cuda_status(
+      hqqk::launch_column_sums(dG, dbias_gate, dU, dbias_up, M, N, x_dtype, stream));
 }

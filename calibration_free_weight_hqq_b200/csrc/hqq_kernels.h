@@ -137,9 +137,10 @@ cudaError_t launch_empty_sums(const void* const (&bias)[2], int mats, int64_t M,
 // dG = dY * U * act'(G), dU = dY * act(G), elementwise over n values of x_dtype.
 cudaError_t launch_gated_grad(const void* dY, const void* G, const void* U, int64_t n, int x_dtype,
                               int act, void* dG, void* dU, cudaStream_t stream);
-// out[c] = sum over rows of A[rows, cols], fp32 in a fixed order, rounded once.
-cudaError_t launch_column_sum(const void* A, int64_t rows, int64_t cols, int x_dtype, void* out,
-                              cudaStream_t stream);
+// out0[c] = sum over rows of A0[rows, cols] and out1 of A1, fp32 in a fixed order, rounded once; those
+// without an out are left.
+cudaError_t launch_column_sums(const void* A0, void* out0, const void* A1, void* out1, int64_t rows,
+                               int64_t cols, int x_dtype, cudaStream_t stream);
 
 // MXFP4: n = rows*cols elements (n % 32 == 0), blocks of 32 consecutive elements.
 cudaError_t launch_mxfp4_quantize(const void* W, int dtype, int64_t n, uint8_t* codes,
