@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
   constexpr bool kWhole = GROUP != 8;
   constexpr int kGroups = 64 / GROUP;            // groups of a lane's codes of a k-block
   constexpr int kGroupsHalf = kGroups > 1 ? kGroups / 2 : 1;
+  constexpr bool kTwos = GROUP == 16 && !ANY;    // meta by two groups
   constexpr int kDepth = few_depth(NBITS, MATS);
   using Tile = CodeTile<NBITS, kFewKB, true>;
   constexpr int kTile = tile_bytes(NBITS, kFewKB);  // a warp's k-block
@@ -203,8 +204,12 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
 #pragma unroll
       for (int i = 0; i < MATS; ++i)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          next[i][r][u] = load_raw_meta<ANY>(slab[i], a.w, step, meta_at[r] + u);
+        for (int r = 0; r < 2; ++r) {
+          if constexpr (!kTwos)
+            next[i][r][u] = load_raw_meta<ANY>(slab[i], a.w, step, meta_at[r] + u);
+          else if (u % 2 == 0)
+            next[i][r][u] = load_raw_meta_two(slab[i], step, meta_at[r] + u);
+        }
     }
   };
   if (warp < KB && blockIdx.x < tiles) {
@@ -234,7 +239,9 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int u = 0; u < kGroups; ++u) {
-              float2 sz = meta_f32_pair<ANY, F16>(next[i][r][u], slab[i], a.w.meta_dt);
+              RawMeta<ANY> raw = next[i][r][u];
+              if constexpr (kTwos) raw = one_of_two(next[i][r][u & ~1], u % 2);
+              float2 sz = meta_f32_pair<ANY, F16>(raw, slab[i], a.w.meta_dt);
               if (tail && kb * kFewKB + 64 * t + GROUP * u >= K)
                 sz = make_float2(0.0f, 0.0f);  // W' = 0 past K
               m[i][r][u] = group_meta<NBITS>(sz.x, sz.y, &one);
@@ -366,7 +373,7 @@ cudaError_t launch_few_typed(const FewJob& j, const FewArgs& a, cudaStream_t st)
     else if (j.group_size == 32)
       kernel = any ? few_tokens_kernel<NBITS, F16, MATS, 32, true>
                    : few_tokens_kernel<NBITS, F16, MATS, 32, false>;
-    else if (j.group_size == 16 && !any)
+    else if (j.group_size == 16 && !any && meta_by_twos(j.w, j.mats))
       kernel = few_tokens_kernel<NBITS, F16, MATS, 16, false>;
   }
   if (smem > 48 * 1024) {

@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   // A thread converts two chunks of 32 codes a stage: 64 in a row, or in the gated form 32 of either
   // weight. Their groups:
   constexpr int kGroups = GROUP >= 32 ? 1 : 32 / GROUP;
+  constexpr bool kTwos = GROUP == 16 && !ANY;  // meta by two groups
   constexpr bool kShared = MODE != kMidGated && GROUP >= 64;  // both chunks lie in one group
   constexpr int kBK = mid_bk(MODE);
   constexpr int kDepth = mid_depth(NBITS, MODE);
@@ -372,8 +373,12 @@ __global__ void __launch_bounds__(kMidThreads, 1)
 #pragma unroll
         for (int u = 0; u < kGroups; ++u) {
           const uint32_t at = col + (MATS == 2 ? 0 : 32 * h) + GROUP * u;
-          if (at < cols)
-            next[h][u] = load_raw_meta<ANY>(slab[MATS == 2 ? h : 0], a.w, 0u, row_meta + (at >> a.w.lg_group));
+          if (at >= cols) continue;
+          const uint32_t group_at = row_meta + (at >> a.w.lg_group);
+          if constexpr (!kTwos)
+            next[h][u] = load_raw_meta<ANY>(slab[MATS == 2 ? h : 0], a.w, 0u, group_at);
+          else if (u % 2 == 0)
+            next[h][u] = load_raw_meta_two(slab[MATS == 2 ? h : 0], 0u, group_at);
         }
       }
     };
@@ -400,7 +405,9 @@ __global__ void __launch_bounds__(kMidThreads, 1)
         for (int h = 0; h < kMeta; ++h)
 #pragma unroll
           for (int u = 0; u < kGroups; ++u) {
-            float2 sz = meta_f32_pair<ANY, F16>(next[h][u], slab[MATS == 2 ? h : 0], a.w.meta_dt);
+            RawMeta<ANY> raw = next[h][u];
+            if constexpr (kTwos) raw = one_of_two(next[h][u & ~1], u % 2);
+            float2 sz = meta_f32_pair<ANY, F16>(raw, slab[MATS == 2 ? h : 0], a.w.meta_dt);
             // W' = 0 outside the weight
             if (!in_row || at0 + (MATS == 2 ? 0 : 32 * h) + GROUP * u >= cols) sz = make_float2(0.0f, 0.0f);
             m[h][u] = group_meta<NBITS>(sz.x, sz.y, &one);
@@ -603,7 +610,7 @@ cudaError_t launch_mid_mode(const MidJob& j, const MidPlan& plan, cudaStream_t s
     else if (j.group_size == 32)
       kernel = any ? mid_tokens_kernel<NBITS, F16, MODE, 32, true>
                    : mid_tokens_kernel<NBITS, F16, MODE, 32, false>;
-    else if (j.group_size == 16 && !any)
+    else if (j.group_size == 16 && !any && meta_by_twos(j.w, j.weights))
       kernel = mid_tokens_kernel<NBITS, F16, MODE, 16, false>;
   }
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
