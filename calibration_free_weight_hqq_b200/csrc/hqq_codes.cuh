@@ -353,7 +353,7 @@ __device__ __forceinline__ Slab slab_of_row(const WeightArgs& a, int i, int64_t 
   b.scale_mm = b.zero_mm = nullptr;
   b.group0 = 0;
   if constexpr (ANY) {
-    const int64_t run0 = g0 / a.meta_run;
+    const int64_t run0 = a.lg_run >= 0 ? g0 >> a.lg_run : g0 / a.meta_run;  // (long division is slow)
     b.group0 = static_cast<uint32_t>(g0 - run0 * a.meta_run);
     if (a.scale_mm[i] != nullptr) b.scale_mm = a.scale_mm[i] + run0;
     if (a.zero_mm[i] != nullptr) b.zero_mm = a.zero_mm[i] + run0;
