@@ -633,18 +633,21 @@ def _check_weights(dtype: torch.dtype, w: QuantizedWeight, up: Optional[Quantize
 
 class _OnStream:
     """A product call on a device or stream that is not the current one. Within it new tensors come
-    from that stream's memory, and the caching allocator is told (record_stream) of inputs used there
-    and of outputs the caller's stream will use, so that neither is handed out again too early."""
+    from that stream's memory, and the caching allocator is told (record_stream) of the call's tensors
+    used there and of outputs the caller's stream will use, so that none is handed out again too
+    early."""
 
-    def __init__(self, w: QuantizedWeight, stream, inputs):
+    def __init__(self, w: QuantizedWeight, stream, used):
         self.caller = torch.cuda.current_stream(w.device)
         self.handle = _stream(stream, w.device)
         self.guards = [torch.cuda.device(w.device)]
         self.other = stream is not None and stream != self.caller
         if self.other:
             self.guards.append(torch.cuda.stream(stream))
-            for t in inputs:
-                t.record_stream(stream)
+            for u in used:
+                for t in u.tensors if isinstance(u, QuantizedWeight) else (u,):
+                    if t is not None and t.is_cuda:
+                        t.record_stream(stream)
         for g in self.guards:
             g.__enter__()
 
@@ -662,12 +665,12 @@ class _OnStream:
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _begin(w: QuantizedWeight, stream, *inputs):
+def _begin(w: QuantizedWeight, stream, *used):
     """(stream handle, None) where the call runs on the current device and stream, else (handle, an
-    _OnStream to leave when the call is enqueued)."""
+    _OnStream to leave when the call is enqueued). used: the call's weights and given tensors."""
     if stream is None and torch.cuda.current_device() == w.index:
         return _current_raw_stream(w.index), None
-    on = _OnStream(w, stream, inputs)
+    on = _OnStream(w, stream, used)
     return on.handle, on
 
 
@@ -723,7 +726,7 @@ def hqq_linear_ex(X: torch.Tensor, w: QuantizedWeight, *, Y: Optional[torch.Tens
     if w.dtype is not None:
         _check_weights(X.dtype, w)
     L = _lib or lib()
-    handle, on = _begin(w, stream, X)
+    handle, on = _begin(w, stream, w, X, Y, workspace)
     try:
         Y = _out(Y, "Y", _shape(X, w.rows), X)
         ws = _workspace(workspace, L.hqq_linear_workspace_bytes(M, w.ptr, 0), w)
@@ -744,7 +747,7 @@ def hqq_linear_backward(dY: torch.Tensor, w: QuantizedWeight, *, bias_grad: bool
     a dbias to write) returns (dX, dbias), dbias the sum of dY over the tokens."""
     M = _tokens(dY, "dY", w.rows, w)
     L = _lib or lib()
-    handle, on = _begin(w, stream, dY)
+    handle, on = _begin(w, stream, w, dY, dX, dbias, workspace)
     try:
         dX = _out(dX, "dX", _shape(dY, w.cols), dY)
         if bias_grad or dbias is not None:
@@ -771,7 +774,7 @@ def hqq_gated_linear(X: torch.Tensor, gate: QuantizedWeight, up: QuantizedWeight
     M = _tokens(X, "X", gate.cols, gate)
     _check_weights(X.dtype, gate, up)
     L = _lib or lib()
-    handle, on = _begin(gate, stream, X)
+    handle, on = _begin(gate, stream, gate, up, X, Y, G, U, workspace)
     try:
         shape = _shape(X, gate.rows)
         Y = _out(Y, "Y", shape, X)
@@ -806,7 +809,7 @@ def hqq_gated_linear_backward(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor
             raise ValueError(f"{name} must be like dY")
         _cuda(t, name, gate.device)
     L = _lib or lib()
-    handle, on = _begin(gate, stream, dY, G, U)
+    handle, on = _begin(gate, stream, gate, up, dY, G, U, dX, dG, dU, workspace)
     dbg = dbu = None
     try:
         dX = _out(dX, "dX", _shape(dY, gate.cols), dY)

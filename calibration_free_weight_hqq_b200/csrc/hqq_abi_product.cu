@@ -2,6 +2,7 @@
 // layers of every format, the gated pair, their gradients): argument validation, the choice of
 // kernel, and the order of the launches. The contract is in include/hqq/hqq.h.
 #include <algorithm>
+#include <initializer_list>
 
 #include "../../include/hqq/hqq.h"
 #include "hqq_abi_internal.h"
@@ -234,6 +235,29 @@ hqq_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   return aligned(workspace, 16) ? HQQ_OK : HQQ_ERR_ALIGNMENT;
 }
 
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+
+// HQQ_ERR_INVALID_ARG where one of the first `outputs` ranges (or the workspace, counted among them)
+// overlaps another range: the kernels read while they write.
+hqq_status check_apart(std::initializer_list<Range> ranges, size_t outputs) {
+  const Range* const r = ranges.begin();
+  for (size_t i = 0; i < outputs; ++i)
+    for (size_t j = i + 1; j < ranges.size(); ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].p), b = reinterpret_cast<uintptr_t>(r[j].p);
+      if (a != 0 && b != 0 && r[i].bytes != 0 && r[j].bytes != 0 && a < b + r[j].bytes &&
+          b < a + r[i].bytes)
+        return HQQ_ERR_INVALID_ARG;
+    }
+  return HQQ_OK;
+}
+
+size_t token_bytes(int64_t M, int64_t width) {
+  return static_cast<size_t>(M) * static_cast<size_t>(width) * 2;
+}
+
 hqq_status forward(const void* X, int64_t M, int dtype, const hqq_weight& w, const hqq_weight* up,
                    int act, void* Y, void* G, void* U, void* workspace, size_t workspace_bytes,
                    cudaStream_t stream) {
@@ -241,7 +265,10 @@ hqq_status forward(const void* X, int64_t M, int dtype, const hqq_weight& w, con
   if (!Y || (w.cols > 0 && !X)) return HQQ_ERR_INVALID_ARG;
   if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(G, 16) || !aligned(U, 16))
     return HQQ_ERR_ALIGNMENT;
-  hqq_status st = check_workspace(workspace, workspace_bytes, forward_need(M, w, up));
+  const size_t need = forward_need(M, w, up), out = token_bytes(M, w.rows);
+  hqq_status st = check_workspace(workspace, workspace_bytes, need);
+  if (st == HQQ_OK)
+    st = check_apart({{Y, out}, {G, out}, {U, out}, {workspace, need}, {X, token_bytes(M, w.cols)}}, 4);
   if (st != HQQ_OK) return st;
   if ((st = check_device(w.cols > 0 ? X : Y)) != HQQ_OK) return st;
   if (w.cols == 0) {
@@ -363,7 +390,11 @@ HQQ_EXPORT hqq_status hqq_linear_backward(const void* dY, int64_t M, hqq_dtype x
   if (!product && !sums) return HQQ_OK;
   if ((product && !dX) || (M > 0 && w->rows > 0 && !dY)) return HQQ_ERR_INVALID_ARG;
   if (!aligned(dY, 16) || !aligned(dX, 16) || !aligned(dbias, 2)) return HQQ_ERR_ALIGNMENT;
-  st = check_workspace(workspace, workspace_bytes, product ? backward_need(M, *w, nullptr) : 0);
+  const size_t need = product ? backward_need(M, *w, nullptr) : 0;
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st == HQQ_OK)
+    st = check_apart({{dX, token_bytes(M, w->cols)}, {dbias, token_bytes(1, w->rows)}, {workspace, need},
+                      {dY, token_bytes(M, w->rows)}}, 3);
   if (st != HQQ_OK) return st;
   if ((st = check_device(dY ? dY : product ? dX : dbias)) != HQQ_OK) return st;
   const void* A[2] = {dY, nullptr};
@@ -391,7 +422,12 @@ HQQ_EXPORT hqq_status hqq_gated_linear_backward(const void* dY, const void* G, c
                         static_cast<const void*>(dX)})
     if (!aligned(p, 16)) return HQQ_ERR_ALIGNMENT;
   if (!aligned(dbias_gate, 2) || !aligned(dbias_up, 2)) return HQQ_ERR_ALIGNMENT;
-  st = check_workspace(workspace, workspace_bytes, product ? backward_need(M, *gate, up) : 0);
+  const size_t need = product ? backward_need(M, *gate, up) : 0, wide = token_bytes(M, N);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st == HQQ_OK)
+    st = check_apart({{dX, token_bytes(M, K)}, {dG, wide}, {dU, wide}, {dbias_gate, token_bytes(1, N)},
+                      {dbias_up, token_bytes(1, N)}, {workspace, need}, {dY, wide}, {G, wide}, {U, wide}},
+                     6);
   if (st != HQQ_OK) return st;
   const void* first = rows ? dY : product ? dX : dbias_gate ? dbias_gate : dbias_up;
   if ((st = check_device(first)) != HQQ_OK) return st;

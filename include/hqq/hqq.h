@@ -368,8 +368,8 @@ typedef enum { HQQ_ACT_SILU = 0, HQQ_ACT_GELU = 1, HQQ_ACT_GELU_TANH = 2 } hqq_a
  *              same shape, their formats may differ.
  *   x_dtype    HQQ_BF16 or HQQ_F16: every activation, gradient and bias of the call.
  *   tensors    device, row-major and dense; activations and gradients 16-byte aligned, biases and
- *              their gradients 2-byte. Outputs must not overlap inputs, the workspace or each
- *              other.
+ *              their gradients 2-byte. Outputs must not overlap activations, the workspace or
+ *              each other (HQQ_ERR_INVALID_ARG otherwise), nor the weights.
  *   workspace  device, 16-byte aligned, at least the bytes the matching *_workspace_bytes call
  *              returns (NULL is fine when that is 0: a few tokens on an axis-1 weight). It holds
  *              dequantized weights during the call; its contents before do not matter and after
@@ -435,9 +435,9 @@ hqq_status hqq_mxfp4_dequantize(const void* codes, const void* scales, int64_t r
                                 int64_t cols, hqq_dtype out_dtype, void* W_out,
                                 cudaStream_t stream);
 
-/* Kernels that wait on barriers inside a CTA (hqq_linear, and the products above when they run
- * on dequantized weights) bound each wait by about two seconds; a wait that runs out sets the CTA's outputs aside (not written), frees its
- * resources and is counted. *count receives the number counted since the library was
+/* Kernels that wait on barriers inside a CTA (hqq_linear, and the products above from 9 tokens
+ * on) bound each wait by about two seconds; a wait that runs out sets the CTA's outputs aside (not
+ * written), frees its resources and is counted. *count receives the number counted since the library was
  * loaded on the current device (0 on every healthy run). Synchronises the device. */
 hqq_status hqq_wait_timeouts(unsigned int* count);
 

@@ -163,3 +163,29 @@ def test_struct_mirror_matches_the_header():
     """The struct's size: six pointers, two 64-bit sizes and hqq_params (13 4-byte fields), padded."""
     assert ctypes.sizeof(hqq.HQQParams) == 52
     assert ctypes.sizeof(hqq.HQQWeight) == 6 * 8 + 2 * 8 + 56
+
+
+def test_overlapping_tensors_are_refused(L):
+    """An output may overlap neither activations, nor the workspace, nor another output."""
+    w = weight(rows=256, cols=512, axis=0)       # dequantized: it needs a workspace
+    M, MB = 4, 1 << 20
+    far = [FAKE + i * 64 * MB for i in range(12)]
+    for back in range(-4 * 256 * 2 + 16, 4 * 512 * 2, 512):      # X [4, 512] against Y [4, 256]
+        assert linear(L, w, X=far[0], Y=far[0] + back, ws=far[1]) == INVALID
+    assert linear(L, w, X=far[0], Y=far[1], ws=far[1] + 1024) == INVALID
+    assert grad(L, w, dY=far[0], dX=far[0], ws=far[1]) == INVALID
+    assert grad(L, w, dY=far[0], dX=far[2], db=far[2] + 16, ws=far[1]) == INVALID
+    assert gated(L, w, w, X=far[0], Y=far[1], G=far[1], U=far[2], ws=far[3]) == INVALID
+    assert gated(L, w, w, X=far[0], Y=far[1], G=far[2], U=far[0], ws=far[3]) == INVALID
+    names = ("dY", "G", "U", "dG", "dU", "dX", "dbg", "dbu", "ws")
+    apart = dict(zip(names, far))
+    for out in ("dG", "dU", "dX", "dbg", "dbu", "ws"):
+        for other in names:
+            if other != out:
+                assert gated_grad(L, w, w, **{**apart, out: apart[other]}) == INVALID, (out, other)
+    # apart, and touching end to start: only the device is missing
+    end = FAKE + M * 512 * 2
+    assert linear(L, w, X=FAKE, Y=end, ws=far[1]) == linear(L, w, X=far[0], Y=far[2], ws=far[1]) != INVALID
+    assert gated_grad(L, w, w, **apart) != INVALID
+    # the same token tensor as two inputs, and one weight as gate and up, are fine
+    assert gated_grad(L, w, w, **{**apart, "G": apart["dY"], "U": apart["dY"]}) != INVALID
