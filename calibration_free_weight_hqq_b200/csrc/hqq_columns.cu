@@ -4,11 +4,13 @@
 // The codes of a row block of G rows lie column by column, G of a column side by side; W' is wanted
 // row by row. A block takes 128 columns of one row block, one contiguous piece of the code stream: it
 // comes in by 16-byte loads, waits in shared memory (columns padded to an odd number of words) and
-// goes out with a warp writing 64 neighbouring columns, 128 bytes, of a row at a time. Bound: HBM, 2
-// bytes written and nbits / 8 read per code. Measured, 4 bits, group 64: 4096 x 11008 in 27 us (4.2 TB/s
-// of the 6.5 a copy reaches), where the kernel that writes one code per lane takes 218 us; 3 bits, 4096 x
-// 4096 in 18.6 us, bound by the division of a slot by the ten codes of a word. The arithmetic and its
-// three roundings are the dequantizer's.
+// goes out with a warp writing 64 neighbouring columns, 128 bytes, of a row at a time. Bound: the
+// instructions of a code (issue slots 72 % taken), then HBM, 2 bytes written and nbits / 8 read per
+// code. Measured, 4096 x 11008, against the kernel that writes one code per lane: 4 bits, group 64, 27 us
+// (4.2 TB/s of the 6.5 a copy reaches) against 218; 2 bits, group 256, 20 against 215; 8 bits, group 64, 30
+// against 227, group 16, whose blocks have 16 rows only, 58 against 215; 3 bits, 4096 x 4096, 18 against 68.
+// Four columns a thread were slower (32 us at 4 bits): shared memory reads then conflict. The
+// arithmetic and its three roundings are the dequantizer's.
 #include "hqq_device.cuh"
 #include "hqq_kernels.h"
 
