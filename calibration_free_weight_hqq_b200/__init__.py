@@ -708,6 +708,11 @@ def _nbytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+# Up to this many tokens a forward call mostly needs no workspace: it is made without one first, and
+# again where the library refuses (asking for the size before took 0.4 us of 8.7 at the smallest).
+_FEW = 8
+_NEEDS_WORKSPACE = 6
+
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
@@ -729,9 +734,14 @@ def hqq_linear_ex(X: torch.Tensor, w: QuantizedWeight, *, Y: Optional[torch.Tens
     handle, on = _begin(w, stream, w, X, Y, workspace)
     try:
         Y = _out(Y, "Y", _shape(X, w.rows), X)
-        ws = _workspace(workspace, L.hqq_linear_workspace_bytes(M, w.ptr, 0), w)
-        st = L.hqq_linear_ex(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), w.ptr, Y.data_ptr(),
-                             _ptr(ws), _nbytes(ws), handle)
+        st = _NEEDS_WORKSPACE
+        if M <= _FEW and workspace is None:
+            st = L.hqq_linear_ex(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), w.ptr, Y.data_ptr(),
+                                 None, 0, handle)
+        if st == _NEEDS_WORKSPACE:
+            ws = _workspace(workspace, L.hqq_linear_workspace_bytes(M, w.ptr, 0), w)
+            st = L.hqq_linear_ex(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), w.ptr, Y.data_ptr(),
+                                 _ptr(ws), _nbytes(ws), handle)
     finally:
         if on is not None:
             on.leave(Y)
@@ -780,11 +790,16 @@ def hqq_gated_linear(X: torch.Tensor, gate: QuantizedWeight, up: QuantizedWeight
         Y = _out(Y, "Y", shape, X)
         if save or G is not None or U is not None:
             G, U = _out(G, "G", shape, X), _out(U, "U", shape, X)
-        ws = _workspace(workspace,
-                        L.hqq_gated_linear_workspace_bytes(M, gate.ptr, up.ptr, 0), gate)
-        st = L.hqq_gated_linear(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), gate.ptr, up.ptr,
-                                code, Y.data_ptr(), _ptr(G), _ptr(U), _ptr(ws), _nbytes(ws),
-                                handle)
+        st = _NEEDS_WORKSPACE
+        if M <= _FEW and workspace is None:
+            st = L.hqq_gated_linear(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), gate.ptr, up.ptr,
+                                    code, Y.data_ptr(), _ptr(G), _ptr(U), None, 0, handle)
+        if st == _NEEDS_WORKSPACE:
+            ws = _workspace(workspace,
+                            L.hqq_gated_linear_workspace_bytes(M, gate.ptr, up.ptr, 0), gate)
+            st = L.hqq_gated_linear(X.data_ptr(), M, _TORCH_DT.get(X.dtype, -1), gate.ptr, up.ptr,
+                                    code, Y.data_ptr(), _ptr(G), _ptr(U), _ptr(ws), _nbytes(ws),
+                                    handle)
     finally:
         if on is not None:
             on.leave(Y, G, U)
