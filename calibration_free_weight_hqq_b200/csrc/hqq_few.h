@@ -40,7 +40,7 @@ __host__ __device__ constexpr size_t few_smem(int nbits, int mats, int warps, in
 // barriers then pass under the other's work: 4 bits, 1 token, 11008 x 4096, 11.3 us against 12.7 with
 // 16 warps, gated 21.1 against 23.6, 28672 x 8192 45.8 against 49.7; equal at 8 tokens), else 16; 0
 // where X does not fit at all, or the row length exceeds the kernel's 32-bit offsets inside a tile, or
-// there are more tokens than an MMA takes. (The some-token kernel is slower wherever this one serves:
+// there are more tokens than an MMA takes. (The some-token kernel is slower wherever this one serves at full speed:
 // 11008 x 4096, 8 tokens here 14 us, 24 tokens there 21.5, and its time hardly depends on tokens there.)
 inline int few_warps(const FewJob& j) {
   if (j.M > kFewTokens || j.K > kFewMaxCols) return 0;

@@ -371,7 +371,7 @@ typedef enum { HQQ_ACT_SILU = 0, HQQ_ACT_GELU = 1, HQQ_ACT_GELU_TANH = 2 } hqq_a
  *              their gradients 2-byte. Outputs must not overlap activations, the workspace or
  *              each other (HQQ_ERR_INVALID_ARG otherwise), nor the weights.
  *   workspace  device, 16-byte aligned, at least the bytes the matching *_workspace_bytes call
- *              returns (NULL is fine when that is 0: a few tokens on an axis-1 weight). It holds
+ *              returns (NULL is fine when that is 0: a few tokens on most axis-1 weights). It holds
  *              dequantized weights during the call; its contents before do not matter and after
  *              are undefined. Two calls that use one workspace at the same time race, captured
  *              graphs that are replayed concurrently included.
