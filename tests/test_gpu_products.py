@@ -642,3 +642,53 @@ def test_more_than_2_pow_32_codes(N, K):
     dY = torch.zeros(len(rows), N, dtype=torch.bfloat16, device="cuda")
     dY[torch.arange(len(rows), device="cuda"), rows] = 1.0
     assert torch.equal(hqq.hqq_linear_backward(dY, w).double(), W)
+
+
+@pytest.mark.parametrize("M", [1, 40, 600])
+def test_a_weight_dropped_after_a_call_on_another_stream(M):
+    """Its memory is not handed out again before that stream is done."""
+    L = Layer(264, 320, 4, 64, 1, "bf16", bias=True, seed=M)
+    X, _ = draw((M, 320), M, "bf16")
+    want = hqq.hqq_linear_ex(X, L.h)
+    torch.cuda.synchronize()
+    pk, sc, zr, b = (t.clone() for t in L.h.tensors)
+    sizes = [(t.shape, t.dtype) for t in (pk, sc, zr, b)]
+    w = hqq.quantized_weight((pk, sc, zr), 264, 320, L.params, bias=b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    Y = hqq.hqq_linear_ex(X, w, stream=side)
+    del w, pk, sc, zr, b
+    for shape, dtype in sizes:
+        torch.full(shape, 77, dtype=dtype, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("nbits", NBITS)
+def test_groups_of_16_on_odd_elements(nbits):
+    """Scale and zero that cannot be loaded two groups at a time."""
+    N, K = 72, 512
+    L = Layer(N, K, nbits, 16, 1, "bf16", seed=nbits)
+
+    def shifted(t):
+        return torch.cat([t.new_zeros(1), t.reshape(-1)])[1:]
+
+    pk, sc, zr = L.h.tensors[:3]
+    w = hqq.quantized_weight((pk, shifted(sc), shifted(zr)), N, K, L.params)
+    for M in (1, 8, 40):
+        X, _ = draw((M, K), M, "bf16")
+        dY, _ = draw((M, N), M, "bf16")
+        assert torch.equal(hqq.hqq_linear_ex(X, w), hqq.hqq_linear_ex(X, L.h))
+        assert torch.equal(hqq.hqq_gated_linear(X, w, L.h), hqq.hqq_gated_linear(X, L.h, L.h))
+        assert torch.equal(hqq.hqq_linear_backward(dY, w), hqq.hqq_linear_backward(dY, L.h))
+
+
+@pytest.mark.parametrize("M", [1, 8, 33])
+@pytest.mark.parametrize("nbits,meta", [(2, "u8"), (3, "u8scale"), (4, "f32"), (8, "u8zero"), (1, "f16")])
+def test_gated_in_groups_of_16_with_other_meta(nbits, meta, M):
+    N, K = 136, 512
+    gate, up = (Layer(N, K, nbits, 16, 1, "bf16", meta, seed=nbits + i) for i in (0, 50))
+    X, X64 = draw((M, K), M, "bf16", scale=0.02)
+    check_gated(M, N, K, "silu", "bf16", gate, up, X, X64)
