@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
     uint8_t* stage = smem + kOffOut + static_cast<uint32_t>(warp - 2) * kBlocks * kBlockBytes;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     int n = 0;
+    uint32_t stored = 0;  // blocks of this warp, over all its tiles
     for (int tile = pair; tile < tiles; tile += pairs, ++n) {
       const uint32_t acc = n & 1;
       const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_cl(bar(kAccFull + acc), (n >> 1) & 1,
@@ -348,9 +349,11 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
             }
             o[i / 2] = pack2_16<OUT>(v0, v1);
           }
+          // The last store may still be read, so the slots alternate by stored blocks: by c, the first block
+          // of a tile would take the slot of a tile's last one that N cut off at an even c.
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
-          if (in) store_block<OUT>(&map_d, stage + (c & 1) * kBlockBytes, lane, o, nc, row0);
+          if (in) store_block<OUT>(&map_d, stage + (stored++ & 1) * kBlockBytes, lane, o, nc, row0);
         }
       }
       tc_fence_before();

@@ -692,3 +692,43 @@ def test_gated_in_groups_of_16_with_other_meta(nbits, meta, M):
     gate, up = (Layer(N, K, nbits, 16, 1, "bf16", meta, seed=nbits + i) for i in (0, 50))
     X, X64 = draw((M, K), M, "bf16", scale=0.02)
     check_gated(M, N, K, "silu", "bf16", gate, up, X, X64)
+
+
+# ------------------------------------------------------------------ many tiles for every CTA pair
+
+def in_parts(call, *tensors, rows=4096):
+    """The call on blocks of the tokens, one after the other: its outputs, joined."""
+    parts = [call(*(t[m:m + rows].contiguous() for t in tensors)) for m in range(0, len(tensors[0]), rows)]
+    return [torch.cat(p) for p in zip(*parts)]
+
+
+def close_on_device(got, A, W, L, dtype, what):
+    """Every element of got = A W^T in 64 bits, on the GPU."""
+    A, W = A.double(), torch.from_numpy(W).cuda()
+    want, u = A @ W.T, UNIT[dtype]
+    tol = u * want.abs() + (1 + u) * L * 2.0 ** -23 * (A.abs() @ W.abs().T) + TINY[dtype]
+    assert ((got.double() - want).abs() <= tol).all(), what
+
+
+@pytest.mark.parametrize("N", [1056, 2312, 2784])
+@pytest.mark.parametrize("K", [64, 256])
+def test_every_row_of_many_tiles_with_a_ragged_last_column(N, K):
+    """32 row blocks of 256 tokens: a CTA pair goes on from a tile that N cuts off after an odd number of
+    32-column blocks to others, with so short a contraction that nothing else holds it up. Bit for bit
+    what calls of 4096 tokens give, where no pair does."""
+    M, G = 8192, 8 if N % 32 else 32
+    X, _ = draw((M, K), 1, "bf16", scale=0.3)
+    L, up = (Layer(N, K, 4, 64, 1, "bf16", seed=s) for s in (K, K + 1))
+    back = Layer(K, N, 4, G, 1, "bf16", seed=N)  # dX has N columns
+    for _ in range(3):
+        Y = hqq.hqq_linear_ex(X, L.h)
+        assert torch.equal(Y, in_parts(lambda x: (hqq.hqq_linear_ex(x, L.h),), X)[0])
+        dX = hqq.hqq_linear_backward(X, back.h)
+        assert torch.equal(dX, in_parts(lambda x: (hqq.hqq_linear_backward(x, back.h),), X)[0])
+        pair = hqq.hqq_gated_linear(X, L.h, up.h, save=True)
+        for a, b in zip(pair, in_parts(lambda x: hqq.hqq_gated_linear(x, L.h, up.h, save=True), X)):
+            assert torch.equal(a, b)
+    close_on_device(Y, X, L.W, K, "bf16", "Y")
+    close_on_device(dX, X, back.W.T.copy(), K, "bf16", "dX")
+    close_on_device(pair[1], X, L.W, K, "bf16", "G")
+    close_on_device(pair[2], X, up.W, K, "bf16", "U")
