@@ -17,6 +17,7 @@ constexpr int kFewKB = 256;       // codes of a row per k-block, two chunks of 3
 constexpr int kFewMaxWarps = 16;  // warps of a CTA: 8 (two CTAs an SM) or 16
 constexpr int kFewRedStride = kFewRows + 4;  // floats per token of a partial tile: the stores
                                              // of a fragment fall on 32 different banks
+constexpr int kFewMaxSmem = 226 * 1024;  // dynamic shared memory of a CTA at most
 constexpr int kFewRed = 8 * kFewRedStride * 4;  // bytes of one warp's partial tile
 
 // k-blocks whose codes are in flight per warp: about 6 KB of them, 96 KB an SM at 16 warps (the
@@ -45,7 +46,7 @@ __host__ __device__ constexpr size_t few_smem(int nbits, int mats, int warps, in
 inline int few_warps(const FewJob& j) {
   if (j.M > kFewTokens || j.K > kFewMaxCols) return 0;
   if (few_smem(j.nbits, j.mats, 8, j.M, j.K) <= 113 * 1024) return 8;
-  return few_smem(j.nbits, j.mats, 16, j.M, j.K) <= 226 * 1024 ? 16 : 0;
+  return few_smem(j.nbits, j.mats, 16, j.M, j.K) <= kFewMaxSmem ? 16 : 0;
 }
 
 }  // namespace hqqk

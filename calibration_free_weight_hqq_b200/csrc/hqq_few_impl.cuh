@@ -382,8 +382,10 @@ cudaError_t launch_few_typed(const FewJob& j, const FewArgs& a, cudaStream_t st)
     }
   }
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    // always the most, never this call's: a smaller value, set by another thread between here and the
+    // launch, would have the launch refused
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem);
     if (e != cudaSuccess) return e;
   }
   kernel<<<grid, 32 * warps, smem, st>>>(a);

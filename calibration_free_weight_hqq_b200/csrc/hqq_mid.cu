@@ -29,7 +29,7 @@ bool mid_plan(const MidJob& j, MidPlan* plan) {
   p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms, units / 2)));
   const uint32_t ring = static_cast<uint32_t>(kMidDqWarps * mid_codes(j.nbits, j.mode) * mid_depth(j.nbits, j.mode));
   const uint32_t stage = 2 * kMidTileBytes + static_cast<uint32_t>(p.tok) * 2 * mid_bk(j.mode);
-  p.stages = static_cast<int>(std::min<uint32_t>(4, (232448u - 2048u - ring) / stage));
+  p.stages = static_cast<int>(std::min<uint32_t>(4, (kMidMaxSmem - 2048u - ring) / stage));
   p.off_ring = p.stages * stage;
   p.off_bar = p.off_ring + ring;
   p.smem = p.off_bar + 1024 + 1024;  // barriers, TMEM address and flag; slack to align the base

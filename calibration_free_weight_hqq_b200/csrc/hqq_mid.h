@@ -17,6 +17,7 @@ constexpr int kMidDqWarps = 16;  // two groups of 8 warps, alternate stages
 constexpr int kMidEpiWarps = 4;
 constexpr int kMidThreads = 32 * (2 + kMidDqWarps + kMidEpiWarps);
 constexpr uint32_t kMidTileBytes = kMidRows * kMidLine * 2;  // a 128 x 64 tile of W'
+constexpr int kMidMaxSmem = 232448;  // dynamic shared memory of a CTA at most: all of an SM's 227 KB
 constexpr int64_t kMidMaxCols = int64_t(1) << 24;  // 32-bit offsets inside a tile's 128 rows
 
 enum MidMode : int { kMidLinear = 0, kMidGated = 1, kMidBackward = 2 };

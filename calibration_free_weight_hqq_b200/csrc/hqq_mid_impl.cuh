@@ -614,8 +614,9 @@ cudaError_t launch_mid_mode(const MidJob& j, const MidPlan& plan, cudaStream_t s
       kernel = any || !meta_by_twos(j.w, j.weights) ? mid_tokens_kernel<NBITS, F16, MODE, 16, true>
                                                     : mid_tokens_kernel<NBITS, F16, MODE, 16, false>;
   }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(plan.smem));
+  // always the most, never this call's: a smaller value, set by another thread between here and the
+  // launch, would have the launch refused
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMidMaxSmem);
   if (e != cudaSuccess) return e;
   kernel<<<plan.ctas, kMidThreads, plan.smem, st>>>(x[0], x[1], a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

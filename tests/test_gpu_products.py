@@ -18,6 +18,8 @@ its results are subnormal):
   * act': a sum of terms of at most 8 in size under the same errors: 2^-13 |g|-free absolute bound
     for the tanh form, 2^-15 for the others.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -732,3 +734,37 @@ def test_every_row_of_many_tiles_with_a_ragged_last_column(N, K):
     close_on_device(dX, X, back.W.T.copy(), K, "bf16", "dX")
     close_on_device(pair[1], X, L.W, K, "bf16", "G")
     close_on_device(pair[2], X, up.W, K, "bf16", "U")
+
+
+# ------------------------------------------------------------------ host threads
+
+@pytest.mark.parametrize("sizes", [((8, 1024), (1, 512)), ((16, 1024), (200, 1024))])
+def test_two_host_threads_at_different_sizes(sizes):
+    """Calls of one kernel that want different amounts of shared memory, from two threads at once."""
+    layers = {K: Layer(136, K, 4, 64, 1, "bf16", seed=K) for _, K in sizes}
+    failed = []
+
+    def work(M, K):
+        try:
+            X, _ = draw((M, K), M, "bf16")
+            stream = torch.cuda.Stream()
+            want = hqq.hqq_linear_ex(X, layers[K].h)
+            Y, n = torch.empty_like(want), hqq.hqq_linear_workspace_bytes(M, layers[K].h)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+            torch.cuda.synchronize()
+            args = (X.data_ptr(), M, hqq.HQQ_BF16, layers[K].h.ptr, Y.data_ptr(), ws.data_ptr() if n else None,
+                    n, stream.cuda_stream)
+            call = hqq.lib().hqq_linear_ex  # without the interpreter lock
+            for _ in range(20000):
+                assert call(*args) == 0
+            stream.synchronize()
+            assert torch.equal(Y, want)
+        except BaseException as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=s) for s in sizes]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
