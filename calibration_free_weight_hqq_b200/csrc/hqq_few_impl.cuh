@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
       if constexpr (kWhole) {
         const bool tail = (kb + 1) * kFewKB > K;
         GroupMeta m[MATS][2][kGroups];
-        bool one = !ANY;
+        Exactness known;
 #pragma unroll
         for (int i = 0; i < MATS; ++i)
 #pragma unroll
@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
               float2 sz = meta_f32_pair<ANY, F16>(raw, slab[i], a.w.meta_dt);
               if (tail && kb * kFewKB + 64 * t + GROUP * u >= K)
                 sz = make_float2(0.0f, 0.0f);  // W' = 0 past K
-              m[i][r][u] = group_meta<NBITS>(sz.x, sz.y, &one);
+              m[i][r][u] = group_meta<NBITS, F16>(sz.x, sz.y, &known);
             }
-        one = !ANY && __all_sync(0xFFFFFFFFu, one);
+        const bool one = !ANY && __all_sync(0xFFFFFFFFu, known.holds());
         uint32_t slot[MATS][2];  // 3 bits: the first code's place in its 16 bytes, of both rows
 #pragma unroll
         for (int i = 0; i < MATS; ++i) {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
           for (int i = 0; i < MATS; ++i) {
             Codes32<NBITS> c[2];
             GroupMeta m[2][4];
-            bool one = false;
+            Exactness known;  // not used
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const uint32_t row = r == 0 ? g : row1;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(32 * kFewMaxWarps, 1) few_tokens_kernel(const 
                       load_raw_meta<ANY>(slab[i], a.w, 0u,
                                          row * groups_per_row + ((kh + 8 * u) >> a.w.lg_group)),
                       slab[i], a.w.meta_dt);
-                m[r][u] = group_meta<NBITS>(sz.x, sz.y, &one);
+                m[r][u] = group_meta<NBITS, F16>(sz.x, sz.y, &known);
               }
             }
             multiply_chunk<NBITS, F16, 4, false>(acc[i], c, m[0], m[1], x + 16 * h);

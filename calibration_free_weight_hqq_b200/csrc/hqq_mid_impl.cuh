@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
       const bool in_row = mw.row + r < rows;
       if constexpr (kWhole) {
         GroupMeta m[kMeta][kGroups];
-        bool one = !ANY;
+        Exactness known;
 #pragma unroll
         for (int h = 0; h < kMeta; ++h)
 #pragma unroll
@@ -410,9 +410,9 @@ __global__ void __launch_bounds__(kMidThreads, 1)
             float2 sz = meta_f32_pair<ANY, F16>(raw, slab[MATS == 2 ? h : 0], a.w.meta_dt);
             // W' = 0 outside the weight
             if (!in_row || at0 + (MATS == 2 ? 0 : 32 * h) + GROUP * u >= cols) sz = make_float2(0.0f, 0.0f);
-            m[h][u] = group_meta<NBITS>(sz.x, sz.y, &one);
+            m[h][u] = group_meta<NBITS, F16>(sz.x, sz.y, &known);
           }
-        one = !ANY && __all_sync(0xFFFFFFFFu, one);
+        const bool one = !ANY && __all_sync(0xFFFFFFFFu, known.holds());
         uint32_t first_slot[MATS];  // 3 bits: the row's first code's place in its 16 bytes
 #pragma unroll
         for (int i = 0; i < MATS; ++i)
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
           const Codes32<NBITS> c =
               load_codes_units<NBITS>(b.codes, b.code0 + codes0 + more, static_cast<int>(left));
           GroupMeta m[4];
-          bool one = false;
+          Exactness known;  // not used
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float2 sz = make_float2(0.0f, 0.0f);
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kMidThreads, 1)
               sz = meta_f32_pair<ANY, F16>(
                   load_raw_meta<ANY>(b, a.w, 0u, row_meta + ((at + 8 * u) >> a.w.lg_group)), b,
                   a.w.meta_dt);
-            m[u] = group_meta<NBITS>(sz.x, sz.y, &one);
+            m[u] = group_meta<NBITS, F16>(sz.x, sz.y, &known);
           }
           uint4 o[4];
           dequant_chunk<NBITS, OUT, 4, false>(c, m, o);

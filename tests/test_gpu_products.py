@@ -768,3 +768,30 @@ def test_two_host_threads_at_different_sizes(sizes):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("nbits", NBITS)
+def test_one_hot_with_zeros_beyond_the_reach_of_a_sum(nbits):
+    """Zeros of 2^20 to 2^40 whose products with the scale are ties of bf16: one step of fp32 in
+    code - zero turns W' over."""
+    N, K, G = 64, 4096, 64
+    rng = np.random.default_rng(nbits)
+    z, s = np.meshgrid(np.arange(128, 256), np.arange(128, 256), indexing="ij")
+    p = z * s
+    tie = np.where(p < 1 << 15, p % 128 == 64, p % 256 == 128)
+    pick = rng.integers(0, tie.sum(), N * K // G)
+    e = rng.integers(20 - 7, 41 - 7, pick.size)
+    zero = (z[tie][pick] * 2.0 ** e * rng.choice([-1.0, 1.0], pick.size)).astype(np.float32)
+    scale = (s[tie][pick] * 2.0 ** (-7 - e)).astype(np.float32)
+    codes = rng.integers(0, 2 ** nbits, size=N * K, dtype=np.uint8)
+    W = oracle.round_to_dtype(oracle.dequantize(codes, scale, zero, N, K, G, 1), "bf16")
+    q = [torch.from_numpy(oracle.pack(codes, nbits)).cuda()] + \
+        [torch.from_numpy(v).bfloat16().cuda() for v in (scale, zero)]
+    assert all(np.array_equal(host(t), v) for t, v in zip(q[1:], (scale, zero)))
+    w = hqq.quantized_weight(q, N, K, hqq.make_params(nbits, G, 1, w_dtype=torch.bfloat16))
+    eye = torch.eye(K, dtype=torch.bfloat16, device="cuda")
+    for n in (8, 64):
+        for k0 in range(0, K, n):
+            assert np.array_equal(host(hqq.hqq_linear_ex(eye[k0:k0 + n], w)), W.T[k0:k0 + n])
+    eye = torch.eye(N, dtype=torch.bfloat16, device="cuda")
+    assert np.array_equal(host(hqq.hqq_linear_backward(eye, w)), W)
