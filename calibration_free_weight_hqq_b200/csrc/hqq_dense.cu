@@ -25,7 +25,8 @@
 // 11008 235-240 us (1540-1570 TFLOP/s).
 //
 // Every wait is bounded (about two seconds); on expiry the CTA raises an abort flag, counts the
-// timeout, skips its remaining work, waits (bounded) for its copies in flight and frees its TMEM.
+// timeout, skips its remaining work, waits (bounded) for its copies in flight and frees its TMEM. Its sums of
+// parts are marked as missing, and outputs that need one are not written.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -127,6 +128,15 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint8_t* sta
     tma_store_2d(map, smem_u32(stage), x, y);
     bulk_commit();
   }
+}
+
+// Where the part of a tile's row `row` from column n0 on would go: marked as missing, every four columns.
+template <int PRODUCTS>
+__device__ __forceinline__ void no_part(const DenseArgs& a, int part, int64_t row, int n0, int columns) {
+  if (row >= a.M) return;
+  float* to = a.partial + (static_cast<int64_t>(part) * PRODUCTS * a.M + row) * a.N;
+#pragma unroll 1
+  for (int n = n0; n < n0 + columns && n < a.N; n += 4) to[n] = __uint_as_float(kNoPart);
 }
 
 template <bool F16>
@@ -288,16 +298,22 @@ __global__ void __launch_bounds__(dense::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     int n = 0;
     uint32_t stored = 0;  // blocks of this warp, over all its tiles
+    bool lost = false;    // a wait ran out: this and all later tiles
     for (int tile = pair; tile < tiles; tile += pairs, ++n) {
       const uint32_t acc = n & 1;
-      const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_cl(bar(kAccFull + acc), (n >> 1) & 1,
+      lost = lost || !__all_sync(0xFFFFFFFFu, mbar_wait_cl(bar(kAccFull + acc), (n >> 1) & 1,
                                                            abort_flag) &&
                                                   !*abort_flag);
-      if (!ok) break;
-      tc_fence_after();
       int tm, tn;
       tile_coords(tile, args, &tm, &tn);
       const int row0 = tm * kBM + static_cast<int>(rank) * 128 + quarter * 32;
+      if (lost) {
+        if (args.splits == 1) break;
+        no_part<KIND == kDenseGated ? 2 : 1>(args, tile / (args.tiles_m * args.tiles_n), row0 + lane,
+                                             tn * kTileN, kTileN);
+        continue;
+      }
+      tc_fence_after();
       const uint32_t base = tmem + lanes + acc * kBN;
 #pragma unroll 1
       for (int c = 0; c < kTileN / 32; ++c) {
@@ -387,16 +403,19 @@ __global__ void __launch_bounds__(256, 4) dense_finish_kernel(const DenseArgs a)
   for (int64_t at = (blockIdx.x * static_cast<int64_t>(256) + threadIdx.x) * 4; at < plane;
        at += static_cast<int64_t>(gridDim.x) * 1024) {
     float s[kProducts][4] = {};
+    bool whole = true;
     for (int p = 0; p < a.splits; ++p) {
 #pragma unroll
       for (int m = 0; m < kProducts; ++m) {
         const float4 v = __ldcg(reinterpret_cast<const float4*>(a.partial + (p * kProducts + m) * plane + at));
+        if (m == 0) whole = whole && __float_as_uint(v.x) != kNoPart;
         s[m][0] = __fadd_rn(s[m][0], v.x);
         s[m][1] = __fadd_rn(s[m][1], v.y);
         s[m][2] = __fadd_rn(s[m][2], v.z);
         s[m][3] = __fadd_rn(s[m][3], v.w);
       }
     }
+    if (!whole) continue;
     const int n = static_cast<int>(at % a.N);
     float y[4];
 #pragma unroll

@@ -25,7 +25,8 @@
 // one after another: 24 us at 64 tokens, 43 us at 256 (540 TFLOP/s), gated 44 and 77 us; gradient of 4096
 // x 11008 25 and 44 us. Gate and up in one tile share X and meet in the epilogue.
 // Every wait is bounded (about two seconds); on expiry the CTA raises an abort flag, counts the
-// timeout, skips its remaining work, waits for its copies in flight and frees its TMEM.
+// timeout, skips its remaining work, waits for its copies in flight and frees its TMEM. Its partial tiles are
+// marked as missing, and outputs that need one are not written.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -483,20 +484,30 @@ __global__ void __launch_bounds__(kMidThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const uint32_t quarter = warp & 3;  // the TMEM lanes this warp may read
+    const uint32_t row = quarter * 32 + lane;
     uint32_t tile = first / KB, kb = first - tile * KB, left = count;
+    bool lost = false;  // a wait ran out: this and all later sums
     for (uint32_t seg = 0; left > 0; ++seg) {
       const uint32_t n_kb = min(KB - kb, left), buf = seg % bufs;
       const bool whole = n_kb == KB;
-      const bool ok = __all_sync(
-          0xFFFFFFFFu,
-          mbar_wait_idle(bar(kMidAccFull + buf), (seg / bufs) & 1, abort_flag) && !*abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t row = quarter * 32 + lane;
+      lost = lost || !__all_sync(0xFFFFFFFFu, mbar_wait_idle(bar(kMidAccFull + buf), (seg / bufs) & 1,
+                                                             abort_flag) &&
+                                                  !*abort_flag);
       const int n = static_cast<int>(tile / a.p.tok_tiles * kMidRows + row);
       const int64_t tok0 = static_cast<int64_t>(tile % a.p.tok_tiles) * T;
       float* part = a.partial + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * MATS * T *
                                     kMidRows + row;
+      if (lost) {
+        if (!whole) {
+#pragma unroll 1
+          for (uint32_t t = 0; t < T; ++t) part[t * kMidRows] = __uint_as_float(kNoPart);
+        }
+        left -= n_kb;
+        kb = 0;
+        ++tile;
+        continue;
+      }
+      tc_fence_after();
       const uint32_t base = tmem + ((quarter * 32) << 16) + buf * MATS * T;
 #pragma unroll 1
       for (uint32_t t = 0; t < T; t += 16) {
@@ -558,16 +569,19 @@ __global__ void __launch_bounds__(256, 8) mid_finish_kernel(const MidArgs a) {
   for (int m = 0; m < MATS; ++m)
     s[m] = __ldcg(reinterpret_cast<const float4*>(
         a.partial + slot0 * slot + (static_cast<size_t>(m) * T + t) * kMidRows + row));
+  bool whole = __float_as_uint(s[0].x) != kNoPart;  // (one warp writes, or gives up, all four)
 #pragma unroll 2
   for (uint32_t c = c0 + 1; c <= c1; ++c) {
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
       const float4 p = __ldcg(reinterpret_cast<const float4*>(
           a.partial + 2 * c * slot + (static_cast<size_t>(m) * T + t) * kMidRows + row));
+      if (m == 0) whole = whole && __float_as_uint(p.x) != kNoPart;
       s[m] = make_float4(__fadd_rn(s[m].x, p.x), __fadd_rn(s[m].y, p.y), __fadd_rn(s[m].z, p.z),
                          __fadd_rn(s[m].w, p.w));
     }
   }
+  if (!whole) return;
   const float4 g = s[0], u = s[MATS - 1];
   mid_store<F16, MATS>(a, tok, n, g.x, u.x);
   mid_store<F16, MATS>(a, tok, n + 1, g.y, u.y);

@@ -17,6 +17,11 @@ __device__ unsigned int g_wait_timeouts = 0;
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
+// In place of a partial sum that a CTA whose wait ran out did not make: the kernel that adds the parts then
+// leaves the output as it was. A NaN that no sum gives (arithmetic makes 0x7FFFFFFF, and a NaN of a 16-bit
+// input has zeros below).
+constexpr uint32_t kNoPart = 0x7FC05AA5u;
+
 // ---------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -435,10 +435,11 @@ hqq_status hqq_mxfp4_dequantize(const void* codes, const void* scales, int64_t r
                                 int64_t cols, hqq_dtype out_dtype, void* W_out,
                                 cudaStream_t stream);
 
-/* Kernels that wait on barriers inside a CTA (hqq_linear, and the products above from 9 tokens
- * on) bound each wait by about two seconds; a wait that runs out sets the CTA's outputs aside (not
- * written), frees its resources and is counted. *count receives the number counted since the library was
- * loaded on the current device (0 on every healthy run). Synchronises the device. */
+/* Kernels that wait on barriers inside a CTA (hqq_linear, and the products above except forward calls of
+ * up to 8 tokens that need no workspace) bound each wait by about two seconds; a wait that runs out sets
+ * the CTA's outputs aside (not written; nor are those that need a partial sum of it), frees its resources
+ * and is counted. *count receives the number counted since the library was loaded on the current device
+ * (0 on every healthy run). Synchronises the device. */
 hqq_status hqq_wait_timeouts(unsigned int* count);
 
 /* Human-readable name of a status code (static storage). */
