@@ -37,8 +37,10 @@ __device__ __forceinline__ float2 act_and_grad_f32(float g) {
     return make_float2(g * cdf, cdf + g * pdf);
   } else {
     const float s = sigmoid_f32(2.0f * gelu_tanh_arg(g));
-    const float dy = 0.7978845608028654f * (1.0f + 0.134145f * g * g);
-    return make_float2(g * s, s + 2.0f * g * s * (1.0f - s) * dy);
+    // from |g| = 100 on s (1 - s) is 0, and neither 2 g nor g^2, which overflow, must meet it
+    const float c = fminf(fmaxf(g, -100.0f), 100.0f);
+    const float dy = 0.7978845608028654f * (1.0f + 0.134145f * c * c);
+    return make_float2(g * s, s + 2.0f * c * s * (1.0f - s) * dy);
   }
 }
 

@@ -795,3 +795,19 @@ def test_one_hot_with_zeros_beyond_the_reach_of_a_sum(nbits):
             assert np.array_equal(host(hqq.hqq_linear_ex(eye[k0:k0 + n], w)), W.T[k0:k0 + n])
     eye = torch.eye(N, dtype=torch.bfloat16, device="cuda")
     assert np.array_equal(host(hqq.hqq_linear_backward(eye, w)), W)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_derivatives_far_out(act):
+    """Gates so far out that act' is 1 or 0 to more than 64 bits, up to the largest of bf16."""
+    L = Layer(64, 64, 4, 64, 1, "bf16", seed=1)
+    g = torch.tensor([1e3, 1e9, 1e18, 2e19, 1e20, 1e30, 3e38, torch.finfo(torch.bfloat16).max] * 8,
+                     device="cuda").bfloat16().repeat(2, 1)
+    g[1] *= -1
+    dY, _ = draw((2, 64), 1, "bf16", scale=1e-3)
+    u, _ = draw((2, 64), 2, "bf16")
+    dX, dG, dU = hqq.hqq_gated_linear_backward(dY, g, u, L.h, L.h, act)
+    want = (dY.double() * u.double())
+    assert ((dG[0].double() - want[0]).abs() <= 2.0 ** -8 * (1 + 2.0 ** -15) * want[0].abs()).all()
+    assert (dG[1] == 0).all() and (dU[1] == 0).all()
+    assert torch.isfinite(dU).all() and torch.isfinite(dX).all()
