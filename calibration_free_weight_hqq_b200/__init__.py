@@ -661,8 +661,8 @@ class _OnStream:
 
 
 # The handle of a device's current stream; building a torch.cuda.Stream around it first takes 3 us,
-# a quarter of a one-token call.
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+# a quarter of a one-token call. (A torch built without CUDA has none, and no CUDA weight to call with.)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _begin(w: QuantizedWeight, stream, *used):

@@ -2,6 +2,8 @@
 CUDA call (the fake pointers are never dereferenced), the sizes they ask for, and what the binding
 refuses."""
 import ctypes
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -189,3 +191,20 @@ def test_overlapping_tensors_are_refused(L):
     assert gated_grad(L, w, w, **apart) != INVALID
     # the same token tensor as two inputs, and one weight as gate and up, are fine
     assert gated_grad(L, w, w, **{**apart, "G": apart["dY"], "U": apart["dY"]}) != INVALID
+
+
+def test_the_package_imports_with_a_torch_that_has_no_cuda():
+    """Such a torch lacks the CUDA functions of torch._C; a call then refuses its tensors."""
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_getCurrent")]:
+    delattr(torch._C, name)
+import calibration_free_weight_hqq_b200 as hqq
+t = torch.zeros(1, 64, dtype=torch.bfloat16)
+try:
+    hqq.quantized_weight((t, t, t), 8, 64, hqq.make_params(1, 64, 1))
+except ValueError as e:
+    print("refused:", e)
+"""
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "refused:" in run.stdout, run.stderr
