@@ -21,6 +21,7 @@ import ctypes
 import math
 import os
 import threading
+import warnings
 from typing import Optional
 
 import torch
@@ -631,6 +632,12 @@ def _check_weights(dtype: torch.dtype, w: QuantizedWeight, up: Optional[Quantize
         raise ValueError(f"the weights are on {w.device} and {up.device}")
 
 
+def _no_graph(call: str, gradient: str):
+    warnings.warn(f"{call} does not record its input for autograd: its outputs carry no gradient. Call it "
+                  f"from a torch.autograd.Function whose backward is {gradient}, or under torch.no_grad().",
+                  stacklevel=3)
+
+
 class _OnStream:
     """A product call on a device or stream that is not the current one. Within it new tensors come
     from that stream's memory, and the caching allocator is told (record_stream) of the call's tensors
@@ -726,8 +733,11 @@ def hqq_linear_ex(X: torch.Tensor, w: QuantizedWeight, *, Y: Optional[torch.Tens
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Forward pass of a quantized linear layer in any format: Y = X @ W'.T (+ w's bias), X
     [..., cols] bf16 or fp16. A few tokens are multiplied straight from the packed codes; more
-    take a workspace (hqq_linear_workspace_bytes; allocated here when not given)."""
+    take a workspace (hqq_linear_workspace_bytes; allocated here when not given). Autograd records
+    nothing (a warning says so where X asks for it): the gradient is hqq_linear_backward."""
     M = _tokens(X, "X", w.cols, w)
+    if X.requires_grad and torch.is_grad_enabled():
+        _no_graph("hqq_linear_ex", "hqq_linear_backward")
     if w.dtype is not None:
         _check_weights(X.dtype, w)
     L = _lib or lib()
@@ -779,9 +789,12 @@ def hqq_gated_linear(X: torch.Tensor, gate: QuantizedWeight, up: QuantizedWeight
                      workspace: Optional[torch.Tensor] = None, stream=None):
     """The gated pair of projections of a feed-forward block: Y = act(X @ Wg'.T (+ bias)) *
     (X @ Wu'.T (+ bias)), act "silu", "gelu" or "gelu_tanh". With save (or G and U to write)
-    returns (Y, G, U), the projections that hqq_gated_linear_backward needs."""
+    returns (Y, G, U), the projections that hqq_gated_linear_backward needs. Autograd records
+    nothing (a warning says so where X asks for it)."""
     code = _act(act)
     M = _tokens(X, "X", gate.cols, gate)
+    if X.requires_grad and torch.is_grad_enabled():
+        _no_graph("hqq_gated_linear", "hqq_gated_linear_backward")
     _check_weights(X.dtype, gate, up)
     L = _lib or lib()
     handle, on = _begin(gate, stream, gate, up, X, Y, G, U, workspace)

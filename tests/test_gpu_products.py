@@ -19,6 +19,7 @@ its results are subnormal):
     for the tanh form, 2^-15 for the others.
 """
 import threading
+import warnings
 
 import numpy as np
 import pytest
@@ -811,3 +812,40 @@ def test_derivatives_far_out(act):
     assert ((dG[0].double() - want[0]).abs() <= 2.0 ** -8 * (1 + 2.0 ** -15) * want[0].abs()).all()
     assert (dG[1] == 0).all() and (dU[1] == 0).all()
     assert torch.isfinite(dU).all() and torch.isfinite(dX).all()
+
+
+# ------------------------------------------------------------------ autograd
+
+def test_an_input_that_requires_a_gradient_is_not_dropped_silently():
+    L = Layer(64, 128, 4, 64, 1, "bf16", seed=1)
+    X, _ = draw((3, 128), 1, "bf16")
+    want = hqq.hqq_linear_ex(X, L.h)
+    calls = (lambda x: hqq.hqq_linear_ex(x, L.h), lambda x: hqq.hqq_gated_linear(x, L.h, L.h))
+    for call in calls:
+        with pytest.warns(UserWarning, match="no gradient"):
+            call(X.clone().requires_grad_())
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        for call in calls:
+            call(X)
+            with torch.no_grad():
+                call(X.clone().requires_grad_())
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, w):
+            ctx.w = w
+            return hqq.hqq_linear_ex(X, w)
+
+        @staticmethod
+        def backward(ctx, dY):
+            return hqq.hqq_linear_backward(dY.contiguous(), ctx.w), None
+
+    leaf = X.clone().requires_grad_()
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        Y = Linear.apply(leaf, L.h)
+        assert torch.equal(Y, want)
+        dY, _ = draw((3, 64), 2, "bf16")
+        Y.backward(dY)
+    assert torch.equal(leaf.grad, hqq.hqq_linear_backward(dY, L.h))
