@@ -133,8 +133,10 @@ hqqk::MidJob mid_job(int mode, int64_t M, const hqq_weight& w, const hqq_weight*
 //   * dequantized: 0.57 us for a million codes, then waves of 256 x 256 tiles over 74 CTA pairs at
 //     0.33 us for 64 of the contraction, and the partial sums of a product of few tiles.
 // The constants fit 480 pairs of measured times (four products, weights of 4096 x 4096, 4096 x 11008,
-// 11008 x 4096 and 1024 x 8192, 1 to 8 bits, 24 to 768 tokens) to 9 % and 5 %; the route taken is on
-// average 0.5 % slower than the better one. Measured in us, 4 bits, 11008 x 4096 forward and
+// 11008 x 4096 and 1024 x 8192, 1 to 8 bits, 24 to 768 tokens, all at groups of 64 with 16-bit scale and
+// zero) to 9 % and 5 %; there the route taken is on average 0.5 % slower than the better one. Other formats
+// are not told apart and were not fitted: from the codes, groups of 16 and 8-bit meta take longer than
+// estimated, and groups of 8 and rows that are not whole 16-byte pieces several times as long. Measured in us, 4 bits, 11008 x 4096 forward and
 // 4096 x 11008 backward for the first two rows, 11008 x 4096 for the others, codes / dequantized:
 //   tokens       64        256         333         512         768
 //   linear       24 / 50   43 / 50     62 / 72     80 / 73   102 / 74

@@ -22,7 +22,8 @@
 // Where tiles are few the contraction is cut into parts, whose sums a second kernel adds in order.
 // What bounds it: the tensor cores, and in long runs the power limit. Measured, 4096 tokens: gated 11008
 // x 4096 480-500 us (1480-1540 TFLOP/s, 0.91-0.94 of the library product's burst), gradient of 4096 x
-// 11008 235-240 us (1540-1570 TFLOP/s).
+// 11008 235-240 us (1540-1570 TFLOP/s); in a long row of calls, less the other kernels, 588-593 and 288 us
+// (1250-1285 TFLOP/s, 0.91-0.93 of the rate that the library product holds for seconds).
 //
 // Every wait is bounded (about two seconds); on expiry the CTA raises an abort flag, counts the
 // timeout, skips its remaining work, waits (bounded) for its copies in flight and frees its TMEM. Its sums of

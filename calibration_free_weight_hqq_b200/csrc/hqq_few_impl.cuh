@@ -19,8 +19,9 @@
 //   * Codes come by asynchronous copies a few k-blocks ahead (across tiles too), each warp its own;
 //     scale and zero one k-block ahead in registers.
 //   * Lanes without a token of their own (g >= M) repeat the last one; those results are dropped.
-// What bounds it: instructions, three to a code and lane, then their latency: at 16 warps an SM (the
-// registers hold no more) 55 % of the issue slots are taken. Measured, group 64: 11008 x 4096, 4 bits, 1
+// What bounds it: instructions (4.35 a code and lane at 4 bits and 1 token, 7.8 at 3 bits with 8-bit meta and
+// 5 tokens), then their latency: at 16 warps an SM (the registers hold no more) 49 and 67 % of the issue
+// slots are taken. Measured, group 64: 11008 x 4096, 4 bits, 1
 // token 11 us (2.3 TB/s; its bytes take 3.9 us at a copy's rate), the gated pair 21 us; 28672 x 8192, 4
 // bits, 1 token 46 us (2.9 TB/s), 3 bits with 8-bit scale and zero, 5 tokens 86 us.
 #pragma once

@@ -20,7 +20,7 @@
 //     adds them in order (deterministic).
 //   * Codes come by asynchronous copies some stages ahead, each warp its own 16 rows; scale and zero
 //     one stage ahead in registers.
-// What bounds it: the converting warps (55 % of the issue slots, the tensor core waits for them) and at
+// What bounds it: the converting warps (48-68 % of the issue slots, the tensor core waits for them) and at
 // 256 tokens, where two stages fit, the wait of one for the other. Measured, 4 bits, group 64, 11008 x 4096,
 // one after another: 24 us at 64 tokens, 43 us at 256 (540 TFLOP/s), gated 44 and 77 us; gradient of 4096
 // x 11008 25 and 44 us. Gate and up in one tile share X and meet in the epilogue.
